@@ -58,6 +58,11 @@ class NF4WeightStruct(ctypes.Structure):
     ]
 
 
+class EpilogueStruct(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p)]
+
+
 class NF4KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
 
@@ -71,6 +76,7 @@ def _load() -> ctypes.CDLL:
     vp, i64, i32, f32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
     u64 = ctypes.c_uint64
     W = ctypes.POINTER(NF4WeightStruct)
+    EP = ctypes.POINTER(EpilogueStruct)
     sig = {
         "nf4_quantize": ([vp, W, vp], ctypes.c_int),
         "nf4_quantize_typed": ([vp, i32, W, vp], ctypes.c_int),
@@ -97,6 +103,12 @@ def _load() -> ctypes.CDLL:
         "qlora_merge": ([W, vp, vp, i32, f32, vp, i32, vp], ctypes.c_int),
         "qlora_multi_lora_fwd": ([W, vp, i64, vp, vp, i32, i32, ctypes.POINTER(f32), vp, vp, vp, sz,
                                   vp], ctypes.c_int),
+        "qlora_linear_fwd_epilogue": ([W, vp, i64, vp, vp, i32, f32, EP, vp, vp, vp, vp, sz, vp],
+                                      ctypes.c_int),
+        "qlora_fwd_epilogue_workspace_bytes": ([i64, i64, i64, i32], sz),
+        "qlora_bwd_epilogue_workspace_bytes": ([i64, i64, i64, i32], sz),
+        "qlora_linear_bwd_epilogue": ([W, vp, i64, vp, vp, i32, f32, EP, vp, vp, vp, vp, vp, vp, vp, vp,
+                                       i32, vp, sz, vp], ctypes.c_int),
         "nf4_device_status": ([vp], ctypes.c_int),
         "nf4_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "nf4_profiling": ([i32], ctypes.c_int),
@@ -526,6 +538,113 @@ def qlora_linear_bwd_dropout_philox(qw: QuantizedWeight, x: torch.Tensor, A: tor
                                                _stream(x.device)),
            "qlora_linear_bwd_dropout_philox")
     return dX, dA, dB
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3, "gelu": 4}   # nf4_act
+
+
+def _act(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _on(device: torch.device):
+    """The device made current for a call (the library launches on the current one)."""
+    return torch.cuda.device(device)
+
+
+def _epilogue(qw: QuantizedWeight, M: int, act: str, bias, mul, residual) -> EpilogueStruct:
+    if bias is not None:
+        _check_t("bias", bias, (qw.n,), torch.bfloat16, qw.device)
+    for name, t in (("mul", mul), ("residual", residual)):
+        if t is not None:
+            _check_t(name, t, (M, qw.n), torch.bfloat16, qw.device)
+    p = lambda t: None if t is None else t.data_ptr()
+    return EpilogueStruct(_act(act), p(bias), p(mul), p(residual))
+
+
+def qlora_linear_fwd_epilogue(qw: QuantizedWeight, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                              alpha: float, bias: Optional[torch.Tensor] = None, act: str = "none",
+                              mul: Optional[torch.Tensor] = None,
+                              residual: Optional[torch.Tensor] = None, save_u: bool = True,
+                              save_z: bool = True, h: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None):
+    """The layer with its epilogue in the same kernels:
+    z = x W~^T + (alpha/r)(x A^T) B^T + bias, h = act(z) * mul + residual, rounded
+    once. bias [n], mul and residual [M, n], bf16, each optional; act is a key of
+    ACTIVATIONS. h may be the residual (or mul) itself. Returns (h, u, z) with
+    u = x A^T (fp32) if save_u and the pre-activation z (bf16) if save_z: what
+    qlora_linear_bwd_epilogue takes. For act "relu" with save_z the sum is formed
+    more exactly, at twice the products (see the C header). workspace: at least
+    fwd_epilogue_workspace_bytes."""
+    M, r = _layer_args(qw, x, A, B)
+    ep = _epilogue(qw, M, act, bias, mul, residual)
+    if h is not None:
+        _check_t("h", h, (M, qw.n), torch.bfloat16, qw.device)
+    _check_ws(workspace, qw.device)
+    _need_cuda(x, A, B)
+    with _on(qw.device):
+        if h is None:
+            h = torch.empty(M, qw.n, dtype=torch.bfloat16, device=x.device)
+        u = torch.empty(M, r, dtype=torch.float32, device=x.device) if save_u else None
+        z = torch.empty(M, qw.n, dtype=torch.bfloat16, device=x.device) if save_z else None
+        ws = workspace if workspace is not None else _workspace(
+            fwd_epilogue_workspace_bytes(M, qw.n, qw.k, r), x.device)
+        s = qw.struct()
+        _check(lib.qlora_linear_fwd_epilogue(ctypes.byref(s), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha),
+                                             ctypes.byref(ep), _ptr(h), _ptr(z), _ptr(u), _ptr(ws), ws.numel(),
+                                             _stream(x.device)), "qlora_linear_fwd_epilogue")
+    return h, u, z
+
+
+def fwd_epilogue_workspace_bytes(M: int, n: int, k: int, r: int) -> int:
+    return int(lib.qlora_fwd_epilogue_workspace_bytes(M, n, k, r))
+
+
+def bwd_epilogue_workspace_bytes(M: int, n: int, k: int, r: int) -> int:
+    return int(lib.qlora_bwd_epilogue_workspace_bytes(M, n, k, r))
+
+
+def qlora_linear_bwd_epilogue(qw: QuantizedWeight, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                              alpha: float, dH: torch.Tensor, z: Optional[torch.Tensor] = None,
+                              act: str = "none", mul: Optional[torch.Tensor] = None,
+                              u: Optional[torch.Tensor] = None, need_dX: bool = True,
+                              need_dbias: bool = False, grad_dtype: torch.dtype = torch.bfloat16,
+                              workspace: Optional[torch.Tensor] = None):
+    """(dX, dA, dB, dbias, dmul) of qlora_linear_fwd_epilogue; dX is None when
+    need_dX is False, dbias when need_dbias is False, dmul when there is no mul.
+    z and u are what the forward returned (z may be None for act "none" without
+    mul; u is recomputed when None). The residual's gradient is dH itself.
+    grad_dtype (bf16 or fp32) is the dtype of dA, dB and dbias."""
+    M, r = _layer_args(qw, x, A, B)
+    ep = _epilogue(qw, M, act, None, mul, None)
+    _check_t("dH", dH, (M, qw.n), torch.bfloat16, qw.device)
+    if z is not None:
+        _check_t("z", z, (M, qw.n), torch.bfloat16, qw.device)
+    elif act != "none" or mul is not None:
+        raise ValueError("z (the forward's pre-activation) is required")
+    if u is not None:
+        _check_t("u", u, (M, r), torch.float32, qw.device)
+    if grad_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("adapter gradients are bf16 or fp32")
+    _check_ws(workspace, qw.device)
+    _need_cuda(x, A, B, dH)
+    with _on(qw.device):
+        dX = torch.empty(M, qw.k, dtype=torch.bfloat16, device=x.device) if need_dX else None
+        dA = torch.empty(r, qw.k, dtype=grad_dtype, device=x.device)
+        dB = torch.empty(qw.n, r, dtype=grad_dtype, device=x.device)
+        dbias = torch.empty(qw.n, dtype=grad_dtype, device=x.device) if need_dbias else None
+        dmul = torch.empty(M, qw.n, dtype=torch.bfloat16, device=x.device) if mul is not None else None
+        ws = workspace if workspace is not None else _workspace(
+            bwd_epilogue_workspace_bytes(M, qw.n, qw.k, r), x.device)
+        s = qw.struct()
+        _check(lib.qlora_linear_bwd_epilogue(ctypes.byref(s), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha),
+                                             ctypes.byref(ep), _ptr(dH), _ptr(z), _ptr(u), _ptr(dX), _ptr(dA),
+                                             _ptr(dB), _ptr(dbias), _ptr(dmul), int(grad_dtype == torch.float32),
+                                             _ptr(ws), ws.numel(), _stream(x.device)),
+               "qlora_linear_bwd_epilogue")
+    return dX, dA, dB, dbias, dmul
 
 
 def device_status(device=None) -> int:

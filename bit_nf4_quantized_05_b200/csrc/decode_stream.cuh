@@ -33,7 +33,7 @@
 // from bf16(s_b * level) * x by at most one bf16 rounding of each term.
 #pragma once
 
-#include "nf4_common.cuh"
+#include "epilogue.cuh"
 
 namespace nf4 {
 
@@ -84,6 +84,9 @@ struct DsGroups {
     int ngroups;
     float gscale[16];
 };
+
+// The output step: none, or EpiArgs (bias, activation, mul, residual).
+struct DsNoEpi {};
 
 // Table lookup by shared address. The table is written once before a
 // barrier and never again, and every lookup address is derived from code
@@ -158,11 +161,14 @@ struct DsScales {
 // chunk c goes to ring slot c % 2, and the other slot takes chunk c + 1 as soon as
 // every lane has read chunk c.
 // GT: DsNoGroups, or DsGroups for per-token adapter selection.
-template <int TG, int CB, class GT>
+// ET: DsNoEpi, or EpiArgs: lane j of a row's half-warp finishes token j, with
+// its operands fetched at the start of the tile.
+template <int TG, int CB, class GT, class ET>
 __global__ void __launch_bounds__(kDsThreads, 1)
 qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N, K/2] u8, box {32 CB, 32}
-                           const DecodeArgs a, const GT grp) {
+                           const DecodeArgs a, const GT grp, const ET epi) {
     constexpr bool GROUPS = sizeof(GT) > 1;
+    constexpr bool EPI = sizeof(ET) > 1;
     extern __shared__ __align__(1024) uint8_t dsm[];
     constexpr uint32_t kSlot = 1024u * CB;           // bytes of one chunk (32 rows x 32 CB)
     constexpr uint32_t kRowStride = 32u * CB;        // bytes per row in a slot
@@ -328,6 +334,15 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
             bq[i] = (fn < Nrows && q < a.r)
                         ? __uint_as_float(static_cast<uint32_t>(__ldg(a.B + static_cast<int64_t>(fn) * a.r + q)) << 16)
                         : 0.0f;
+        }
+        float e_bias = 0.0f, e_mul = 1.0f, e_res = 0.0f, e_sum = 0.0f;
+        if constexpr (EPI) {
+            if (fn < Nrows && fj < a.M) {
+                const int64_t o = static_cast<int64_t>(fj) * a.N + fn;
+                if (epi.bias) e_bias = bf16_at(epi.bias + fn);
+                if (epi.mul) e_mul = bf16_at(epi.mul + o);
+                if (epi.residual) e_res = bf16_at(epi.residual + o);
+            }
         }
 #pragma unroll
         for (int rg = 0; rg < 2; ++rg)
@@ -496,9 +511,26 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
                 v += __shfl_xor_sync(0xffffffffu, v, 1);
-                if (fj == 0 && fn < Nrows) {
+                if constexpr (EPI) {
+                    if (fj == m) e_sum = v;            // every lane holds the sum
+                } else if (fj == 0 && fn < Nrows) {
                     __nv_bfloat16 hb = __float2bfloat16_rn(v);
                     a.h[static_cast<int64_t>(m) * a.N + fn] = *reinterpret_cast<uint16_t *>(&hb);
+                }
+            }
+            if constexpr (EPI) {
+                if (fn < Nrows && fj < a.M) {
+                    const int64_t o = static_cast<int64_t>(fj) * a.N + fn;
+                    const float z = e_sum + e_bias;
+                    if (epi.z) {
+                        __nv_bfloat16 zb = __float2bfloat16_rn(z);
+                        epi.z[o] = *reinterpret_cast<uint16_t *>(&zb);
+                    }
+                    float hv = act_value(z, epi.act);
+                    if (epi.mul) hv *= e_mul;
+                    if (epi.residual) hv += e_res;
+                    __nv_bfloat16 hb = __float2bfloat16_rn(hv);
+                    a.h[o] = *reinterpret_cast<uint16_t *>(&hb);
                 }
             }
         }

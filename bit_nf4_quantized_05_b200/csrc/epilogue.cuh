@@ -1,0 +1,230 @@
+// epilogue.cuh -- the element-wise end of the QLoRA layer and its gradient:
+//
+//   forward    z = (the layer's sum) + bias,  h = act(z) . mul + residual
+//   backward   dz = dH . mul . act'(z),  dmul = dH . act(z),  dbias = sum_m dz
+//
+// The forward part runs inside the kernels that produce the sum (the fused
+// GEMM's and the decode kernel's output step), on the fp32 accumulator, before
+// its one rounding to bf16. The backward part is the kernel below: its dz
+// feeds the layer's backward products.
+#pragma once
+
+#include "nf4_common.cuh"
+
+namespace nf4 {
+
+struct EpiArgs {
+    int act;                    // nf4_act
+    const uint16_t *bias;       // [N] bf16 (optional)
+    const uint16_t *mul;        // [M, N] bf16 (optional)
+    const uint16_t *residual;   // [M, N] bf16 (optional)
+    uint16_t *z;                // [M, N] bf16 pre-activation for the backward (optional)
+};
+
+// ---------------------------------------------------------------------------
+// Activations in fp32. The logistic function comes from the hardware
+// exponential and division (a few 2^-22 relative), far inside the bf16
+// rounding of every result; both GELU forms go through functions that keep
+// their relative accuracy for large negative z (no 1 + tanh or 1 + erf
+// cancellation). NaN passes through every activation.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+constexpr float kGeluTanhScale = 1.59576912160573f;    // 2 sqrt(2 / pi)
+constexpr float kGeluTanhCubic = 0.044715f;
+
+__device__ __forceinline__ float act_value(float z, int act) {
+    switch (act) {
+        case NF4_ACT_RELU: return z < 0.0f ? 0.0f : z;
+        case NF4_ACT_SILU: return z * logistic(z);
+        // (1 + tanh(v / 2)) / 2 = logistic(v)
+        case NF4_ACT_GELU_TANH:
+            return z * logistic(kGeluTanhScale * fmaf(kGeluTanhCubic * z * z, z, z));
+        case NF4_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+        default: return z;
+    }
+}
+
+// act(z) and act'(z)
+__device__ __forceinline__ void act_pair(float z, int act, float &a, float &da) {
+    switch (act) {
+        case NF4_ACT_RELU:
+            a = z < 0.0f ? 0.0f : z;
+            da = z > 0.0f ? 1.0f : 0.0f;
+            return;
+        case NF4_ACT_SILU: {
+            const float p = logistic(z);
+            a = z * p;
+            da = fmaf(a, 1.0f - p, p);
+            return;
+        }
+        case NF4_ACT_GELU_TANH: {
+            const float p = logistic(kGeluTanhScale * fmaf(kGeluTanhCubic * z * z, z, z));
+            a = z * p;
+            // p (1 - p) is zero in fp32 long before |z| = 100; the bound keeps z^2 finite
+            const float zz = fminf(z * z, 1.0e4f);
+            da = fmaf(a * (1.0f - p), kGeluTanhScale * fmaf(3.0f * kGeluTanhCubic, zz, 1.0f), p);
+            return;
+        }
+        case NF4_ACT_GELU: {
+            const float cdf = 0.5f * erfcf(-0.70710678118654752f * z);
+            a = z * cdf;
+            da = fmaf(z, 0.39894228040143268f * __expf(-0.5f * z * z), cdf);
+            return;
+        }
+        default:
+            a = z;
+            da = 1.0f;
+    }
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float bf16_at(const uint16_t *p) {
+    return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+}
+__device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
+    __nv_bfloat162 h2 = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&h2);
+}
+__device__ __forceinline__ uint4 bf16_pack8(const float (&f)[8]) {
+    return make_uint4(bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3]), bf16_pack(f[4], f[5]), bf16_pack(f[6], f[7]));
+}
+__device__ __forceinline__ void bf16_unpack8(const uint4 &v, float (&f)[8]) {
+    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// The output step on eight consecutive columns [col, col + 8) of one row: f
+// comes as the fp32 sum and leaves as h. mul and residual may be the output
+// itself: the thread that reads an element is the one that then writes it, so
+// these are plain loads.
+__device__ __forceinline__ void epilogue8(const EpiArgs &e, int row, int N, int col, float (&f)[8]) {
+    const int64_t o = static_cast<int64_t>(row) * N + col;
+    uint4 mv, rv;
+    if (e.mul) mv = *reinterpret_cast<const uint4 *>(e.mul + o);
+    if (e.residual) rv = *reinterpret_cast<const uint4 *>(e.residual + o);
+    if (e.bias) {
+        float b[8];
+        bf16_unpack8(__ldg(reinterpret_cast<const uint4 *>(e.bias + col)), b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] += b[i];
+    }
+    if (e.z) *reinterpret_cast<uint4 *>(e.z + o) = bf16_pack8(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = act_value(f[i], e.act);
+    if (e.mul) {
+        float m[8];
+        bf16_unpack8(mv, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= m[i];
+    }
+    if (e.residual) {
+        float r[8];
+        bf16_unpack8(rv, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] += r[i];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dz = dH . mul . act'(z) (bf16, the operand of the backward's products),
+// dmul = dH . act(z), dbias = sum over tokens of dz (summed in fp32 before the
+// rounding of dz).
+//
+// Bound by HBM: reads dH, z (and mul), writes dz (and dmul), once. A CTA takes
+// 128 columns (16 lanes of 8) and every (32 x splits)-th row from its own; the
+// splits of one column stripe are a cluster, so the column sums meet in
+// distributed shared memory and are added in a fixed order: one launch, no
+// atomics, no workspace. dz is null when there is neither activation nor mul
+// (then dz is dH itself and only the column sums are formed).
+// ---------------------------------------------------------------------------
+constexpr int kEbThreads = 512;
+constexpr int kEbCols = 128;
+constexpr int kEbRows = kEbThreads / (kEbCols / 8);     // rows of one pass of a CTA
+constexpr int kEbMaxSplits = 8;
+
+struct EpiBwdArgs {
+    int64_t M, N;
+    int act;
+    const uint16_t *dH, *z, *mul;   // z, mul optional
+    uint16_t *dz, *dmul;            // optional
+    void *dbias;                    // optional, bf16 or fp32
+    int dbias_f32;
+};
+
+__global__ void __launch_bounds__(kEbThreads)
+qlora_epilogue_bwd_kernel(const EpiBwdArgs a) {
+    __shared__ float part[kEbRows][kEbCols + 4];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int c8 = threadIdx.x & 15, r = threadIdx.x >> 4;
+    const int64_t col = static_cast<int64_t>(blockIdx.y) * kEbCols + c8 * 8;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kEbRows;
+    float sum[8] = {};
+    if (col < a.N) {
+#pragma unroll 2
+        for (int64_t m = static_cast<int64_t>(blockIdx.x) * kEbRows + r; m < a.M; m += step) {
+            const int64_t o = m * a.N + col;
+            float g[8];
+            bf16_unpack8(__ldg(reinterpret_cast<const uint4 *>(a.dH + o)), g);
+            if (a.dz || a.dmul) {
+                uint4 mv = make_uint4(0, 0, 0, 0), zv = mv;
+                if (a.z) zv = __ldg(reinterpret_cast<const uint4 *>(a.z + o));
+                if (a.mul) mv = __ldg(reinterpret_cast<const uint4 *>(a.mul + o));
+                float z[8], f[8], dm[8];
+                bf16_unpack8(zv, z);
+                bf16_unpack8(mv, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float v, d;
+                    act_pair(z[e], a.act, v, d);
+                    dm[e] = g[e] * v;
+                    if (a.mul) g[e] *= f[e];
+                    g[e] *= d;
+                }
+                if (a.dmul) *reinterpret_cast<uint4 *>(a.dmul + o) = bf16_pack8(dm);
+                if (a.dz) *reinterpret_cast<uint4 *>(a.dz + o) = bf16_pack8(g);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += g[e];
+        }
+    }
+    if (!a.dbias) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[r][c8 * 8 + e] = sum[e];
+    __syncthreads();
+    // the CTA's 32 row sums of each column, in row order
+    float v = 0.0f;
+    if (threadIdx.x < kEbCols) {
+#pragma unroll
+        for (int i = 0; i < kEbRows; ++i) v += part[i][threadIdx.x];
+        part[0][threadIdx.x] = v;
+    }
+    // the grid's x dimension is one cluster: its CTAs' sums, in rank order
+    cluster_sync();
+    if (blockIdx.x == 0 && threadIdx.x < kEbCols) {
+        const int64_t n = static_cast<int64_t>(blockIdx.y) * kEbCols + threadIdx.x;
+        const uint32_t own = smem_u32(&part[0][threadIdx.x]);
+        for (uint32_t rk = 1; rk < gridDim.x; ++rk) {
+            float w;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(mapa_shared(own, rk)) : "memory");
+            v += w;
+        }
+        if (n < a.N) {
+            if (a.dbias_f32) {
+                static_cast<float *>(a.dbias)[n] = v;
+            } else {
+                const __nv_bfloat16 b = __float2bfloat16_rn(v);
+                static_cast<uint16_t *>(a.dbias)[n] = *reinterpret_cast<const uint16_t *>(&b);
+            }
+        }
+    }
+    cluster_sync();       // no CTA leaves while its sums may still be read
+}
+
+}  // namespace nf4

@@ -40,7 +40,7 @@
 // taking every G-th stage).
 #pragma once
 
-#include "nf4_common.cuh"
+#include "epilogue.cuh"
 
 namespace nf4 {
 
@@ -77,8 +77,9 @@ struct GemmArgs {
     int *flags;         // [pairs][2][4 epilogue warps], zero at launch; 1 = rows written
     float *D32;         // when non-null: the fp32 result goes here instead of D
     int bshift;         // log2(block size / 64): block of step j is j >> bshift
+    EpiArgs epi;        // the output step of the EPI instantiations
+    int twice;          // EPI: every reduction step also with what rounding the operand left
 };
-
 
 template <int BN, bool DGRAD, int G>
 struct PairCfg {
@@ -244,7 +245,19 @@ __device__ __forceinline__ void set_flag_gpu(int *flag) {
 
 // OUT32: the result is written in fp32 to args.D32 (for a later kernel that
 // adds to it and rounds once) instead of bf16 to args.D.
-template <int BN, bool DGRAD, int G, bool OUT32>
+// EPI: the output step applies args.epi (bias, activation, mul, residual) to
+// the fp32 sum before it is rounded. mul and residual rows are requested into
+// L2 while the tile's products still run: an output thread reads 32 bytes of
+// its row per 16 columns, and sixteen such reads from HBM in a row would take
+// longer than the tile.
+// EPI with args.twice: each reduction step is followed by a second one on the
+// same activations with the rest of the weight, bf16(w - bf16(w)), and each
+// adapter step by one with the rest of the rank-r activations, so that the sum
+// has the weight to 2^-17 rather than 2^-9. A gradient that jumps at z = 0
+// needs that: an error d in z turns the sign of a share d / (3 std(z)) of the
+// elements, and each of those is wrong by its whole size (at 5120 x 5120, one
+// pass left dX 3.2% off in the 2-norm, two leave it at its output's rounding).
+template <int BN, bool DGRAD, int G, bool OUT32, bool EPI = false>
 __global__ void __launch_bounds__(PairCfg<BN, DGRAD, G>::kThreads, 1)
 qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red] bf16, box {64,128}
                        const __grid_constant__ CUtensorMap tm_codes,  // [Nw, K/2] u8, box {32, rows}
@@ -317,7 +330,10 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
 
     const int m_pairs = (args.M + 2 * kBM - 1) / (2 * kBM);
     const int total_tiles = m_pairs * args.n_tiles;
-    const int nsteps = args.main_steps + args.lora_steps;
+    // reduction step `it` is step it >> ps of the operands; its low bit selects the rest
+    const int ps = EPI ? args.twice : 0;
+    const int main_steps = args.main_steps << ps;
+    const int nsteps = main_steps + (args.lora_steps << ps);
     PairSched sched;
     sched.init(nsteps, total_tiles, npairs, pair, args.sk);
     PairSeg sg;
@@ -341,17 +357,17 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
                                        static_cast<uint32_t>(v / kConsumedBars) & 1u, abort_flag))
                             goto done;
                     }
-                    if (it >= args.main_steps && !la_ready) {
+                    if (it >= main_steps && !la_ready) {
                         griddep_wait();
                         la_ready = true;
                     }
                     if (rank == 0) mbar_arrive_expect_tx(&a_full[sa], 2 * Cfg::kABytes);
-                    if (it < args.main_steps)
+                    if (it < main_steps)
                         tma_load_2d_pair(slot_a + sa * Cfg::kABytes, &tm_act, full0 + 8u * sa,
-                                         it * kBK, m0);
-                    else
+                                         (it >> ps) * kBK, m0);
+                    else     // the rests are rows [M, 2M)
                         tma_load_2d_pair(slot_a + sa * Cfg::kABytes, &tm_la, full0 + 8u * sa,
-                                         (it - args.main_steps) * kBK, m0);
+                                         ((it - main_steps) >> ps) * kBK, (it - main_steps) & ps ? m0 + args.M : m0);
                     ++na;
                     if (++sa == SA) sa = 0;
                 }
@@ -369,10 +385,10 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
                 for (int it = sg.k0; it < sg.k1; ++it) {
                     if (!mbar_wait(&c_empty[sc], pc ^ 1, abort_flag)) goto done;
                     uint8_t *c = slot_c + sc * Cfg::kCBytes;
-                    if (it < args.main_steps) {
+                    if (it < main_steps) {
                         mbar_arrive_expect_tx(&c_full[sc], Cfg::kCBytes);
                         if (!DGRAD) {
-                            tma_load_2d(c, &tm_codes, &c_full[sc], it * (kBK / 2), nh);
+                            tma_load_2d(c, &tm_codes, &c_full[sc], (it >> ps) * (kBK / 2), nh);
                         } else {
 #pragma unroll
                             for (int kb = 0; kb < BH / 64; ++kb)
@@ -444,6 +460,17 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
             const bool tail = sg.k0 > 0;
             const bool head = !tail && sg.k1 < nsteps;
             const int rloc = q * 32 + lane;               // row within this CTA's 128
+            if constexpr (EPI) {
+                if (!tail && m0 + rloc < args.M) {
+                    const int64_t o = static_cast<int64_t>(m0 + rloc) * args.out + n0;
+#pragma unroll
+                    for (int c = 0; c < BN; c += 64)       // 128 bytes
+                        if (n0 + c < args.out) {
+                            if (args.epi.mul) prefetch_l2(args.epi.mul + o + c);
+                            if (args.epi.residual) prefetch_l2(args.epi.residual + o + c);
+                        }
+                }
+            }
             if (!mbar_wait(&acc_full[ab], aph, abort_flag)) goto done;
             tc_fence_after();
             if (tail) {
@@ -516,6 +543,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
                                     f4[1] = make_float4(f[4], f[5], f[6], f[7]);
                                     continue;
                                 }
+                                if constexpr (EPI) epilogue8(args.epi, row, args.out, col, f);
                                 uint32_t p[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
@@ -595,9 +623,9 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
             if (moved) p.item = item_of(p.tile);
         };
         auto block_of = [&](const Pos &p) -> int64_t {
-            if (p.tile >= total_tiles || p.it >= args.main_steps || p.item < 0) return -1;
+            if (p.tile >= total_tiles || p.it >= main_steps || p.item < 0) return -1;
             const int64_t bpr = args.kblocks >> args.bshift;      // blocks per W row
-            if (!DGRAD) return p.item * bpr + (p.it >> args.bshift);
+            if (!DGRAD) return p.item * bpr + ((p.it >> ps) >> args.bshift);
             const int64_t wrow = static_cast<int64_t>(p.it) * kBK + r_loc;
             return wrow < args.Nw ? wrow * bpr + (p.item >> args.bshift) : -1;
         };
@@ -627,7 +655,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
         int sb = grp, sc = grp;
         uint32_t pc = 0;
         while (u < nunits) {
-            const bool main = cur.it < args.main_steps;
+            const bool main = cur.it < main_steps;
 
             if (!mbar_wait(&c_full[sc], pc, abort_flag)) goto done;
             // this item's 64 codes go to registers, which frees the code slot
@@ -658,7 +686,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
                 *reinterpret_cast<uint4 *>(brow + ((c ^ swz) << 4)) = make_uint4(w0, w1, w2, w3);
             };
             if (main) {
-                const BlockLut L = make_block_lut(s);
+                const BlockLut L = EPI && (cur.it & ps) ? make_block_lut_rest(s) : make_block_lut(s);
                 const uint32_t words[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
 #pragma unroll
                 for (int wd = 0; wd < 8; ++wd) {
@@ -670,7 +698,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
                 // LoRA stage: the adapter tile comes straight from global memory
                 //   forward: B[nh + i][64 ls .. +64)           (zero beyond r, N)
                 //   dgrad:   A[64 ls + r_loc][64 item .. +64)  (zero beyond r, K)
-                const int ls = cur.it - args.main_steps;
+                const int ls = (cur.it - main_steps) >> ps;
                 const uint16_t *src = nullptr;
                 int nvalid = 0;   // valid 8-element chunks
                 if (cur.item >= 0) {

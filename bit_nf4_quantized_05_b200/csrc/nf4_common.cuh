@@ -417,6 +417,16 @@ struct BlockLut {
     uint32_t hi[4];   // hi[q] bytes: high bytes of entries 4q..4q+3
 };
 
+__device__ __forceinline__ BlockLut block_lut_planes(const uint32_t (&pair)[8]) {
+    BlockLut L;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        L.lo[q] = __byte_perm(pair[2 * q], pair[2 * q + 1], 0x6420);
+        L.hi[q] = __byte_perm(pair[2 * q], pair[2 * q + 1], 0x7531);
+    }
+    return L;
+}
+
 __device__ __forceinline__ BlockLut make_block_lut(float s) {
     uint32_t pair[8];
 #pragma unroll
@@ -426,13 +436,22 @@ __device__ __forceinline__ BlockLut make_block_lut(float s) {
         __nv_bfloat162 p = __floats2bfloat162_rn(s * c_levels[2 * i], s * c_levels[2 * i + 1]);
         pair[i] = *reinterpret_cast<uint32_t *>(&p);
     }
-    BlockLut L;
+    return block_lut_planes(pair);
+}
+
+// What that rounding left: bf16(s * level - bf16(s * level)). The two tables
+// together hold the fp32 weight to 2^-17.
+__device__ __forceinline__ BlockLut make_block_lut_rest(float s) {
+    uint32_t pair[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        L.lo[q] = __byte_perm(pair[2 * q], pair[2 * q + 1], 0x6420);
-        L.hi[q] = __byte_perm(pair[2 * q], pair[2 * q + 1], 0x7531);
+    for (int i = 0; i < 8; ++i) {
+        const float a = s * c_levels[2 * i], b = s * c_levels[2 * i + 1];
+        __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+        const float2 r = __bfloat1622float2(p);
+        p = __floats2bfloat162_rn(a - r.x, b - r.y);
+        pair[i] = *reinterpret_cast<uint32_t *>(&p);
     }
-    return L;
+    return block_lut_planes(pair);
 }
 
 // PRMT with the selector used as given (a selector nibble with bit 3 set

@@ -51,11 +51,11 @@ nf4_status map_fail(int line) {
 // Optional per-kernel event timing (nf4_profiling / nf4_profile_read)
 // ---------------------------------------------------------------------------
 enum KernelKind {
-    KK_QUANTIZE, KK_DEQUANTIZE, KK_LORA_U, KK_LORA_V, KK_LORA_DBDA, KK_ZERO, KK_GEMM_FWD, KK_GEMM_DGRAD, KK_DECODE, KK_DECODE_U, KK_MERGE, KK_LORA_ADD, KK_COUNT
+    KK_QUANTIZE, KK_DEQUANTIZE, KK_LORA_U, KK_LORA_V, KK_LORA_DBDA, KK_ZERO, KK_GEMM_FWD, KK_GEMM_DGRAD, KK_DECODE, KK_DECODE_U, KK_MERGE, KK_LORA_ADD, KK_EPI_BWD, KK_COUNT
 };
 const char *const kKindNames[KK_COUNT] = {
     "nf4_quantize", "nf4_dequantize", "lora_u", "lora_v", "lora_dB_dA", "zero_fill", "qlora_gemm_fwd", "qlora_gemm_dgrad", "qlora_decode",
-    "decode_lora_u", "qlora_merge", "lora_dX_add"};
+    "decode_lora_u", "qlora_merge", "lora_dX_add", "epilogue_bwd"};
 
 struct ProfRecord {
     int kind;
@@ -256,10 +256,11 @@ struct FwdLayout {
 // us: bf16 rank-r activations; upart: the decode path's partial sums of
 // x A^T (M <= 16 tokens only); flags/partial: stream-K scratch (with_sk =
 // false: the whole-tile schedule, none)
-FwdLayout fwd_layout(int64_t M, int32_t r, int sms, bool with_sk = true) {
+// twice: us also holds the rests of its rounding, in as many rows again
+FwdLayout fwd_layout(int64_t M, int32_t r, int sms, bool with_sk = true, bool twice = false) {
     FwdLayout L{};
     size_t off = 0;
-    L.us = off;   off = align256(off + size_t(M) * r * 2);
+    L.us = off;   off = align256(off + size_t(M) * r * 2 * (twice ? 2 : 1));
     L.upart = off;
     if (M <= 16) off = align256(off + size_t(kDsUCtas) * size_t(M) * r * 4);
     if (with_sk) {
@@ -307,6 +308,7 @@ struct SkinnySpec {
     const uint8_t *keep = nullptr;
     int64_t mx = 0, kx = 0;
     DropRng rng{};                     // the mask drawn from the generator instead of keep
+    uint16_t *out_rest = nullptr;      // what rounding out_bf16 left
 };
 
 // Tensor maps and job fields of one product; splits is the launch's split count.
@@ -331,6 +333,7 @@ bool skinny_job(const SkinnySpec &sp, int RN, int splits, CUtensorMap *ta, CUten
     job->r = sp.r;
     job->out_f32 = sp.out_f32;
     job->out_bf16 = sp.out_bf16;
+    job->out_rest = sp.out_rest;
     job->scale = sp.scale;
     job->transposed = sp.transposed;
     job->mask_mode = sp.mask_mode;
@@ -467,7 +470,7 @@ template <int BN, bool DGRAD, int G>
 nf4_status launch_gemm_pair(const nf4_weight *w, const uint16_t *act, int64_t M, int64_t red,
                             int64_t out, const uint16_t *la, int32_t r, const uint16_t *lb,
                             uint16_t *D, cudaStream_t stream, const SkBuf *sk = nullptr,
-                            float *D32 = nullptr) {
+                            float *D32 = nullptr, const EpiArgs *epi = nullptr, bool twice = false) {
     using Cfg = PairCfg<BN, DGRAD, G>;
     CUtensorMap tm_act, tm_codes, tm_la;
     const int64_t N = w->n, K = w->k;
@@ -479,7 +482,7 @@ nf4_status launch_gemm_pair(const nf4_weight *w, const uint16_t *act, int64_t M,
                         DGRAD ? kBK : Cfg::kBH, CU_TENSOR_MAP_SWIZZLE_32B);
     // no LoRA stage when la is null (the adapter term is added by another kernel)
     if (la)
-        ok = ok && make_map(&tm_la, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, la, r, M, kBK, kBM,
+        ok = ok && make_map(&tm_la, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, la, r, twice ? 2 * M : M, kBK, kBM,
                             CU_TENSOR_MAP_SWIZZLE_128B);
     else
         tm_la = tm_act;
@@ -505,6 +508,8 @@ nf4_status launch_gemm_pair(const nf4_weight *w, const uint16_t *act, int64_t M,
     a.lora_b = lb;
     a.D = D;
     a.D32 = D32;
+    if (epi) a.epi = *epi;
+    a.twice = twice ? 1 : 0;
 
     const int dev = current_device();
     const int cap = pair_capacity<BN, DGRAD, G>(dev);
@@ -522,15 +527,18 @@ nf4_status launch_gemm_pair(const nf4_weight *w, const uint16_t *act, int64_t M,
         a.partial = sk->partial;
         a.flags = sk->flags;
     }
+    auto kern = qlora_gemm_pair_kernel<BN, DGRAD, G, false>;
+    if constexpr (DGRAD) {
+        if (D32) kern = qlora_gemm_pair_kernel<BN, DGRAD, G, true>;
+    } else {
+        if (D32) return NF4_ERR_INVALID_ARG;      // the fp32 result is a dgrad form
+        if (epi) kern = qlora_gemm_pair_kernel<BN, DGRAD, G, false, true>;
+    }
+    if (D32 || epi)      // pair_capacity has set the plain form's attribute
+        NF4_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes));
     LaunchTimer t(DGRAD ? KK_GEMM_DGRAD : KK_GEMM_FWD, stream);
-    const cudaError_t e =
-        D32 ? (cudaFuncSetAttribute(qlora_gemm_pair_kernel<BN, DGRAD, G, true>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes) != cudaSuccess
-                   ? cudaErrorInvalidValue
-                   : launch_ex(qlora_gemm_pair_kernel<BN, DGRAD, G, true>, dim3(static_cast<unsigned>(2 * pairs)),
-                        dim3(Cfg::kThreads), Cfg::kSmemBytes, stream, 2u, tm_act, tm_codes, tm_la, a))
-            : launch_ex(qlora_gemm_pair_kernel<BN, DGRAD, G, false>, dim3(static_cast<unsigned>(2 * pairs)),
-                        dim3(Cfg::kThreads), Cfg::kSmemBytes, stream, 2u, tm_act, tm_codes, tm_la, a);
+    const cudaError_t e = launch_ex(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::kThreads),
+                                    Cfg::kSmemBytes, stream, 2u, tm_act, tm_codes, tm_la, a);
     t.stop();
     if (e != cudaSuccess) return cuda_fail(e, __LINE__);
     NF4_TRY_CUDA(cudaGetLastError());
@@ -538,34 +546,34 @@ nf4_status launch_gemm_pair(const nf4_weight *w, const uint16_t *act, int64_t M,
 }
 
 // One instantiation of the decode kernel per (token groups, chunk blocks,
-// per-token adapter selection).
-template <int TG, int CB, class GT>
+// per-token adapter selection or output step).
+template <int TG, int CB, class GT, class ET>
 cudaError_t launch_decode_stream_t(unsigned grid, cudaStream_t stream, const CUtensorMap &tm,
-                                   const DecodeArgs &a, const GT &grp) {
-    auto k = qlora_decode_stream_kernel<TG, CB, GT>;
+                                   const DecodeArgs &a, const GT &grp, const ET &epi) {
+    auto k = qlora_decode_stream_kernel<TG, CB, GT, ET>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDsDynBytes);
     if (e != cudaSuccess) return e;
-    return launch_ex(k, dim3(grid), dim3(kDsThreads), kDsDynBytes, stream, 0u, tm, a, grp);
+    return launch_ex(k, dim3(grid), dim3(kDsThreads), kDsDynBytes, stream, 0u, tm, a, grp, epi);
 }
 
-template <int TG, class GT>
+template <int TG, class GT, class ET>
 cudaError_t launch_decode_stream_cb(int cb, unsigned grid, cudaStream_t stream, const CUtensorMap &tm,
-                                    const DecodeArgs &a, const GT &grp) {
+                                    const DecodeArgs &a, const GT &grp, const ET &epi) {
     switch (cb) {
-        case 1: return launch_decode_stream_t<TG, 1>(grid, stream, tm, a, grp);
-        case 2: return launch_decode_stream_t<TG, 2>(grid, stream, tm, a, grp);
-        case 3: return launch_decode_stream_t<TG, 3>(grid, stream, tm, a, grp);
-        case 4: return launch_decode_stream_t<TG, 4>(grid, stream, tm, a, grp);
-        case 5: return launch_decode_stream_t<TG, 5>(grid, stream, tm, a, grp);
+        case 1: return launch_decode_stream_t<TG, 1>(grid, stream, tm, a, grp, epi);
+        case 2: return launch_decode_stream_t<TG, 2>(grid, stream, tm, a, grp, epi);
+        case 3: return launch_decode_stream_t<TG, 3>(grid, stream, tm, a, grp, epi);
+        case 4: return launch_decode_stream_t<TG, 4>(grid, stream, tm, a, grp, epi);
+        case 5: return launch_decode_stream_t<TG, 5>(grid, stream, tm, a, grp, epi);
         default: return cudaErrorInvalidValue;
     }
 }
 
-template <class GT>
+template <class GT, class ET = DsNoEpi>
 cudaError_t launch_decode_stream(int tg, int cb, unsigned grid, cudaStream_t stream, const CUtensorMap &tm,
-                                 const DecodeArgs &a, const GT &grp) {
-    return tg == 1 ? launch_decode_stream_cb<1>(cb, grid, stream, tm, a, grp)
-                   : launch_decode_stream_cb<2>(cb, grid, stream, tm, a, grp);
+                                 const DecodeArgs &a, const GT &grp, const ET &epi = ET{}) {
+    return tg == 1 ? launch_decode_stream_cb<1>(cb, grid, stream, tm, a, grp, epi)
+                   : launch_decode_stream_cb<2>(cb, grid, stream, tm, a, grp, epi);
 }
 
 // Forward for M <= 16 tokens: partial sums of u = x A^T on a few SMs, then
@@ -583,7 +591,8 @@ bool decode_shape(const nf4_weight *w, int64_t M, int32_t r) {
 nf4_status launch_decode(const nf4_weight *w, const uint16_t *x, int64_t M, const uint16_t *A,
                          const uint16_t *B, int32_t r, float scale, uint16_t *h, float *u_out,
                          float *upart, cudaStream_t stream, const RowGroups *groups = nullptr,
-                         const uint8_t *keep = nullptr, const DropRng &rng = DropRng{}) {
+                         const uint8_t *keep = nullptr, const DropRng &rng = DropRng{},
+                         const EpiArgs *epi = nullptr) {
     // each of the 16 warps takes rb blocks of every 32-row tile, fetched in
     // chunks of cb blocks (the largest divisor of rb that is at most 5)
     const int64_t kblocks = w->k / kBlock;
@@ -639,6 +648,8 @@ nf4_status launch_decode(const nf4_weight *w, const uint16_t *x, int64_t M, cons
         gr.ngroups = groups->ngroups;
         for (int i = 0; i < groups->ngroups && i < 16; ++i) gr.gscale[i] = groups->gscale[i];
         e = launch_decode_stream(tg, cb, grid, stream, tm_codes, a, gr);
+    } else if (epi) {
+        e = launch_decode_stream(tg, cb, grid, stream, tm_codes, a, DsNoGroups{}, *epi);
     } else {
         e = launch_decode_stream(tg, cb, grid, stream, tm_codes, a, DsNoGroups{});
     }
@@ -683,24 +694,26 @@ template <bool DGRAD>
 nf4_status launch_gemm_auto(const nf4_weight *w, const uint16_t *act, int64_t M, int64_t red,
                             int64_t out, const uint16_t *la, int32_t r, const uint16_t *lb,
                             uint16_t *D, cudaStream_t stream, const SkBuf *sk = nullptr,
-                            float *D32 = nullptr) {
+                            float *D32 = nullptr, const EpiArgs *epi = nullptr, bool twice = false) {
     const int dev = current_device();
     const int pairs = pair_capacity<256, DGRAD, kPairGroups>(dev);
     if (pairs > 0) {
         const int64_t tiles256 = ((M + 2 * kBM - 1) / (2 * kBM)) * ((out + 255) / 256);
         if (sk && tiles256 > pairs)
             return launch_gemm_pair<256, DGRAD, kPairGroups>(w, act, M, red, out, la, r, lb, D,
-                                                             stream, sk, D32);
+                                                             stream, sk, D32, epi, twice);
         switch (pick_pair_bn(M, out, pairs, DGRAD)) {
         case 128:
-            return launch_gemm_pair<128, DGRAD, kPairGroups>(w, act, M, red, out, la, r, lb, D, stream, nullptr, D32);
+            return launch_gemm_pair<128, DGRAD, kPairGroups>(w, act, M, red, out, la, r, lb, D, stream, nullptr, D32,
+                                                             epi, twice);
         case 192:
             if constexpr (!DGRAD)
                 return launch_gemm_pair<192, DGRAD, kPairGroups>(w, act, M, red, out, la, r, lb, D,
-                                                                 stream, nullptr, D32);
+                                                                 stream, nullptr, D32, epi, twice);
             break;
         default:
-            return launch_gemm_pair<256, DGRAD, kPairGroups>(w, act, M, red, out, la, r, lb, D, stream, nullptr, D32);
+            return launch_gemm_pair<256, DGRAD, kPairGroups>(w, act, M, red, out, la, r, lb, D, stream, nullptr, D32,
+                                                             epi, twice);
         }
     }
     // no CTA pair of this kernel can be resident (not the case on a B200)
@@ -930,7 +943,7 @@ size_t qlora_fwd_workspace_bytes(int64_t M, int64_t n, int64_t k, int32_t r) {
 nf4_status fwd_impl(const nf4_weight *w, const uint16_t *x, int64_t M, const uint16_t *A,
                     const uint16_t *B, int32_t r, float alpha, float p, const uint8_t *keep,
                     uint16_t *h, float *u_out, void *workspace, size_t ws_bytes, void *stream,
-                    const DropRng &rng = DropRng{}) {
+                    const DropRng &rng = DropRng{}, const EpiArgs *epi = nullptr) {
     nf4_status st = check_layer(w, x, M, A, B, r, alpha);
     if (st != NF4_OK) return st;
     const bool masked = keep != nullptr || rng.on;
@@ -939,7 +952,11 @@ nf4_status fwd_impl(const nf4_weight *w, const uint16_t *x, int64_t M, const uin
     if (!h) return NF4_ERR_INVALID_ARG;
     if (!aligned16(h) || !aligned16(u_out) || !aligned16(keep)) return NF4_ERR_ALIGNMENT;
     const int sms = num_sms(current_device());
-    const FwdLayout L = fwd_layout(M, r, sms);
+    // a ReLU whose pre-activation is kept for the backward: the sign of z decides
+    // whole gradients, so the sum is formed with the weight's and the rank-r
+    // activations' rounding rests as well (the streaming kernel has no such form)
+    const bool twice = epi && epi->act == NF4_ACT_RELU && epi->z;
+    const FwdLayout L = fwd_layout(M, r, sms, true, twice);
     if (!workspace || ws_bytes < L.total) return NF4_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return NF4_ERR_ALIGNMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -949,13 +966,14 @@ nf4_status fwd_impl(const nf4_weight *w, const uint16_t *x, int64_t M, const uin
                    sk_pairs_max(sms)};
     float scale = alpha / static_cast<float>(r);
     if (masked) scale = scale / (1.0f - p);
-    if (decode_shape(w, M, r))
+    if (decode_shape(w, M, r) && !twice)
         return launch_decode(w, x, M, A, B, r, scale, h, u_out, reinterpret_cast<float *>(ws + L.upart), s,
-                             nullptr, keep, rng);
+                             nullptr, keep, rng, epi);
     // u = x A^T (fp32, optional; under dropout the dropped elements of x are
     // zero) and bf16(scale u) for the up-projection stage; this kernel also
     // clears the GEMM's stream-K flags
     SkinnySpec su{x, M, w->k, Major::K, A, r, w->k, Major::K, r, u_out, u_s, scale, 0};
+    if (twice) su.out_rest = u_s + M * r;
     if (masked) {
         su.mask_mode = 1;
         su.keep = keep;
@@ -965,7 +983,7 @@ nf4_status fwd_impl(const nf4_weight *w, const uint16_t *x, int64_t M, const uin
     }
     st = skinny_launch(KK_LORA_U, &su, 1, s, sk.flags, sk.pairs_max * kSkFlagsPerPair);
     if (st != NF4_OK) return st;
-    return launch_gemm_auto<false>(w, x, M, w->k, w->n, u_s, r, B, h, s, &sk);
+    return launch_gemm_auto<false>(w, x, M, w->k, w->n, u_s, r, B, h, s, &sk, nullptr, epi, twice);
 }
 
 nf4_status qlora_linear_fwd(const nf4_weight *w, const uint16_t *x, int64_t M, const uint16_t *A,
@@ -1261,6 +1279,113 @@ nf4_status qlora_linear_bwd_dropout_philox(const nf4_weight *w, const uint16_t *
     if (!(p >= 0.0f && p < 1.0f)) return NF4_ERR_INVALID_ARG;
     return bwd_impl(w, x, M, A, B, r, alpha, p, nullptr, dY, u, dX, dA, dB, workspace, ws_bytes,
                     stream, false, make_drop_rng(p, seed, offset));
+}
+
+// ---- the layer with its epilogue
+
+// The fields of an epilogue that both directions take.
+nf4_status check_epilogue(const qlora_epilogue *ep) {
+    if (!ep || ep->act < NF4_ACT_NONE || ep->act > NF4_ACT_GELU) return NF4_ERR_INVALID_ARG;
+    if (!aligned16(ep->bias) || !aligned16(ep->mul) || !aligned16(ep->residual)) return NF4_ERR_ALIGNMENT;
+    return NF4_OK;
+}
+
+// Two [M, n] bf16 buffers that share some elements.
+bool overlap(const void *p, const void *q, int64_t elems) {
+    if (!p || !q) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    const uintptr_t bytes = static_cast<uintptr_t>(elems) * 2;
+    return a < b + bytes && b < a + bytes;
+}
+
+size_t qlora_fwd_epilogue_workspace_bytes(int64_t M, int64_t n, int64_t k, int32_t r) {
+    if (M <= 0 || n <= 0 || k <= 0 || r <= 0) return 256;
+    return fwd_layout(M, r, num_sms(current_device()), true, true).total;
+}
+
+nf4_status qlora_linear_fwd_epilogue(const nf4_weight *w, const uint16_t *x, int64_t M,
+                                     const uint16_t *A, const uint16_t *B, int32_t r, float alpha,
+                                     const qlora_epilogue *ep, uint16_t *h, uint16_t *z_out,
+                                     float *u_out, void *workspace, size_t ws_bytes, void *stream) {
+    nf4_status st = check_layer(w, x, M, A, B, r, alpha);
+    if (st != NF4_OK) return st;
+    st = check_epilogue(ep);
+    if (st != NF4_OK) return st;
+    if (!aligned16(z_out)) return NF4_ERR_ALIGNMENT;
+    const int64_t out = M * w->n;
+    // h may be mul or residual itself; z may be neither h nor an input
+    if ((h != ep->mul && overlap(h, ep->mul, out)) || (h != ep->residual && overlap(h, ep->residual, out)) ||
+        overlap(z_out, h, out) || overlap(z_out, ep->mul, out) || overlap(z_out, ep->residual, out))
+        return NF4_ERR_INVALID_ARG;
+    const EpiArgs e{ep->act, ep->bias, ep->mul, ep->residual, z_out};
+    return fwd_impl(w, x, M, A, B, r, alpha, 0.0f, nullptr, h, u_out, workspace, ws_bytes, stream, DropRng{}, &e);
+}
+
+size_t qlora_bwd_epilogue_workspace_bytes(int64_t M, int64_t n, int64_t k, int32_t r) {
+    if (M < 0 || n <= 0 || k <= 0 || r <= 0) return 256;
+    M = std::max<int64_t>(M, 1);
+    return bwd_layout(M, r, num_sms(current_device())).total + align256(size_t(M) * size_t(n) * 2);
+}
+
+nf4_status qlora_linear_bwd_epilogue(const nf4_weight *w, const uint16_t *x, int64_t M,
+                                     const uint16_t *A, const uint16_t *B, int32_t r, float alpha,
+                                     const qlora_epilogue *ep, const uint16_t *dH, const uint16_t *z,
+                                     const float *u, uint16_t *dX, void *dA, void *dB, void *dbias,
+                                     uint16_t *dmul, int32_t grads_f32, void *workspace,
+                                     size_t ws_bytes, void *stream) {
+    nf4_status st = check_layer(w, x, M, A, B, r, alpha);
+    if (st != NF4_OK) return st;
+    st = check_epilogue(ep);
+    if (st != NF4_OK) return st;
+    if (!dA || !dB || (grads_f32 != 0 && grads_f32 != 1)) return NF4_ERR_INVALID_ARG;
+    if (M > 0 && (!dH || (!z && (ep->act != NF4_ACT_NONE || dmul)) || (dmul && !ep->mul)))
+        return NF4_ERR_INVALID_ARG;
+    if (!aligned16(dH) || !aligned16(z) || !aligned16(u) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) ||
+        !aligned16(dbias) || !aligned16(dmul))
+        return NF4_ERR_ALIGNMENT;
+    // dmul is written while dH, z and mul are read
+    const int64_t out = M * w->n;
+    if (overlap(dmul, dH, out) || overlap(dmul, z, out) || overlap(dmul, ep->mul, out)) return NF4_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t N = w->n;
+    const size_t base = bwd_layout(std::max<int64_t>(M, 1), r, num_sms(current_device())).total;
+    const bool scaled = ep->act != NF4_ACT_NONE || ep->mul;      // dz is not dH itself
+    const uint16_t *dz = dH;
+    if (M > 0) {
+        if (!workspace || ws_bytes < base + (scaled ? align256(size_t(M) * size_t(N) * 2) : 0)) return NF4_ERR_WORKSPACE;
+        if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return NF4_ERR_ALIGNMENT;
+    }
+    if ((N + kEbCols - 1) / kEbCols > 65535) return NF4_ERR_UNSUPPORTED_SHAPE;
+    if (dbias || (scaled && M > 0)) {
+        EpiBwdArgs a{};
+        a.M = M;
+        a.N = N;
+        a.act = ep->act;
+        a.dH = dH;
+        a.z = z;
+        a.mul = ep->mul;
+        if (scaled && M > 0) {
+            a.dz = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(workspace) + base);
+            dz = a.dz;
+        }
+        a.dmul = dmul;
+        a.dbias = dbias;
+        a.dbias_f32 = grads_f32;
+        // row splits of a column stripe: with column sums they are one cluster,
+        // without them enough CTAs for two full waves
+        const int64_t stripes = (N + kEbCols - 1) / kEbCols, passes = (M + kEbRows - 1) / kEbRows;
+        const int64_t most = dbias ? kEbMaxSplits
+                                   : std::max<int64_t>(kEbMaxSplits, 4 * num_sms(current_device()) / stripes);
+        const unsigned splits = static_cast<unsigned>(std::max<int64_t>(1, std::min(passes, most)));
+        LaunchTimer t(KK_EPI_BWD, s);
+        const cudaError_t e = launch_ex(qlora_epilogue_bwd_kernel, dim3(splits, static_cast<unsigned>(stripes)),
+                                        dim3(kEbThreads), 0, s, dbias ? splits : 0u, a);
+        t.stop();
+        if (e != cudaSuccess) return cuda_fail(e, __LINE__);
+        NF4_TRY_CUDA(cudaGetLastError());
+    }
+    return bwd_impl(w, x, M, A, B, r, alpha, 0.0f, nullptr, dz, u, dX, dA, dB, workspace, ws_bytes, stream,
+                    grads_f32 != 0);
 }
 
 }  // extern "C"

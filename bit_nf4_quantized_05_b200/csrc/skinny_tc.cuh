@@ -37,6 +37,7 @@ struct SkinnyJob {
     int r;               // output columns actually written (<= RN)
     float *out_f32;      // the sum in fp32 (unscaled): [P][r], or [r][P] when transposed; or null
     uint16_t *out_bf16;  // bf16(scale * sum): [P][r], or [r][P] when transposed; or null
+    uint16_t *out_rest;  // what that rounding left, in bf16, same layout; or null
     float scale;
     int transposed;
     // dropout on x as the A operand (LoRA dropout: the keep mask is an input,
@@ -309,6 +310,10 @@ skinny_cluster_kernel(const __grid_constant__ CUtensorMap tm_a0,
                 }
                 __nv_bfloat16 b = __float2bfloat16_rn(sc * acc);
                 J.out_bf16[o] = *reinterpret_cast<uint16_t *>(&b);
+                if (J.out_rest) {
+                    b = __float2bfloat16_rn(sc * acc - __bfloat162float(b));
+                    J.out_rest[o] = *reinterpret_cast<uint16_t *>(&b);
+                }
             }
         }
     }

@@ -277,6 +277,71 @@ QLORA_API nf4_status qlora_linear_bwd_f32grad(const nf4_weight *w, const uint16_
                                               uint16_t *dX, float *dA, float *dB, void *workspace,
                                               size_t ws_bytes, void *stream);
 
+/* Activations of the layer's epilogue and of the experts below:
+ *   silu z / (1 + exp(-z)); gelu_tanh z / (1 + exp(-2 sqrt(2/pi)(z + 0.044715 z^3)));
+ *   gelu z (1 + erf(z / sqrt 2)) / 2. */
+typedef enum {
+    NF4_ACT_NONE = 0,
+    NF4_ACT_RELU = 1,
+    NF4_ACT_SILU = 2,
+    NF4_ACT_GELU_TANH = 3,
+    NF4_ACT_GELU = 4,
+} nf4_act;
+
+/* What follows the layer's sum. The struct lives in host memory, its arrays are
+ * device memory (bf16); each of them may be NULL.
+ *   bias      [n]
+ *   mul       [M, n]  the other factor of a gated pair (for example the
+ *                     up-projection's output, with this layer the gate)
+ *   residual  [M, n] */
+typedef struct {
+    int32_t act; /* nf4_act */
+    const uint16_t *bias;
+    const uint16_t *mul;
+    const uint16_t *residual;
+} qlora_epilogue;
+
+/* The layer with its epilogue in the same kernels:
+ *     z = x W~^T + (alpha/r)(x A^T) B^T + bias
+ *     h = act(z) . mul + residual
+ * all on the fp32 sum, with one rounding to bf16 at the end. z_out (nullable,
+ * [M, n] bf16) receives z for the backward. h may be the same buffer as mul or
+ * residual (the residual stream updated in place); any other overlap of h or
+ * z_out with mul, residual or each other returns NF4_ERR_INVALID_ARG, and so
+ * do a null ep and an unknown act. workspace: at least
+ * qlora_fwd_epilogue_workspace_bytes(M, n, k, r) bytes, 256-byte aligned.
+ * Otherwise as qlora_linear_fwd, with one difference: for a ReLU with z_out the
+ * sum takes the weight and the rank-r activations to 2^-17 instead of bf16's
+ * 2^-9 (twice the tensor-core work), because the gradient jumps with the sign
+ * of z. No page gives the epilogue: it is the element-wise work that
+ * surrounds the pages' layer in a transformer block. */
+QLORA_API size_t qlora_fwd_epilogue_workspace_bytes(int64_t M, int64_t n, int64_t k, int32_t r);
+QLORA_API nf4_status qlora_linear_fwd_epilogue(const nf4_weight *w, const uint16_t *x, int64_t M,
+                                               const uint16_t *A, const uint16_t *B, int32_t r,
+                                               float alpha, const qlora_epilogue *ep, uint16_t *h,
+                                               uint16_t *z_out, float *u_out, void *workspace,
+                                               size_t ws_bytes, void *stream);
+
+/* Backward of qlora_linear_fwd_epilogue:
+ *     dz = dH . mul . act'(z)      (rounded to bf16 as the products' operand)
+ *     dmul = dH . act(z),  dbias = sum over tokens of dz (before that rounding)
+ *     dX, dA, dB: qlora_linear_bwd of dz;  the residual's gradient is dH itself
+ * ep: act and mul as in the forward (bias and residual are not read). z is the
+ * forward's z_out; it may be NULL when act is none and dmul is not wanted. u as
+ * in qlora_linear_bwd. dX, dbias and dmul may be NULL; dmul needs ep->mul and
+ * must not overlap dH, z or mul (NF4_ERR_INVALID_ARG). With grads_f32 == 1, dA, dB and dbias
+ * are fp32, with 0 bf16. relu'(0) = 0. workspace: at least
+ * qlora_bwd_epilogue_workspace_bytes(M, n, k, r) bytes, 256-byte aligned. M == 0
+ * writes zeros to dA, dB and dbias. */
+QLORA_API size_t qlora_bwd_epilogue_workspace_bytes(int64_t M, int64_t n, int64_t k, int32_t r);
+QLORA_API nf4_status qlora_linear_bwd_epilogue(const nf4_weight *w, const uint16_t *x, int64_t M,
+                                               const uint16_t *A, const uint16_t *B, int32_t r,
+                                               float alpha, const qlora_epilogue *ep,
+                                               const uint16_t *dH, const uint16_t *z, const float *u,
+                                               uint16_t *dX, void *dA, void *dB, void *dbias,
+                                               uint16_t *dmul, int32_t grads_f32, void *workspace,
+                                               size_t ws_bytes, void *stream);
+
 /* Adapter merge for inference without adapters ("QLoRA explained", section
  * "Merging and deploying"; "How Fine-Tuning LLMs with LoRA and QLoRA Works",
  * FAQ on merging: W_new = W + (alpha/r) B A):
