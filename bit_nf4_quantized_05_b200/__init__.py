@@ -109,6 +109,8 @@ def _load() -> ctypes.CDLL:
         "qlora_bwd_epilogue_workspace_bytes": ([i64, i64, i64, i32], sz),
         "qlora_linear_bwd_epilogue": ([W, vp, i64, vp, vp, i32, f32, EP, vp, vp, vp, vp, vp, vp, vp, vp,
                                        i32, vp, sz, vp], ctypes.c_int),
+        "nf4_moe_workspace_bytes": ([i64, i32, i64, i64, i32], sz),
+        "nf4_moe_fwd": ([W, W, vp, i64, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
         "nf4_device_status": ([vp], ctypes.c_int),
         "nf4_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "nf4_profiling": ([i32], ctypes.c_int),
@@ -645,6 +647,52 @@ def qlora_linear_bwd_epilogue(qw: QuantizedWeight, x: torch.Tensor, A: torch.Ten
                                              _ptr(ws), ws.numel(), _stream(x.device)),
                "qlora_linear_bwd_epilogue")
     return dX, dA, dB, dbias, dmul
+
+
+def moe_workspace_bytes(M: int, n_experts: int, hidden: int, ffn: int, top_k: int) -> int:
+    return int(lib.nf4_moe_workspace_bytes(M, n_experts, hidden, ffn, top_k))
+
+
+def nf4_moe_fwd(gate_up: QuantizedWeight, down: QuantizedWeight, x: torch.Tensor, router: torch.Tensor,
+                top_k: int, act: str = "silu", renormalise: bool = True,
+                residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None):
+    """A mixture of NF4 experts for a few tokens (at most 64): the router's top_k
+    experts of each token, out = sum_j w_j (act(x Wg^T) * (x Wu^T)) Wd^T + residual.
+    router [E, hidden] bf16; gate_up stacks the experts' gate and up rows,
+    [E * 2 * ffn, hidden] (per expert: ffn gate rows, then ffn up rows), down
+    their down rows, [E * hidden, ffn]. Returns (out [M, hidden] bf16, ids
+    [M, top_k] int32, weights [M, top_k] fp32); see the C header for the routing
+    rule. out may be the residual itself."""
+    if x.dim() != 2 or router.dim() != 2:
+        raise ValueError("x and router must be 2-D")
+    M, H, E = x.shape[0], gate_up.k, router.shape[0]
+    _check_t("x", x, (M, H), torch.bfloat16, gate_up.device)
+    _check_t("router", router, (E, H), torch.bfloat16, gate_up.device)
+    if not 1 <= top_k <= E:
+        raise ValueError(f"top_k must be between 1 and the {E} experts, got {top_k}")
+    if down.device != gate_up.device:
+        raise ValueError(f"down is on {down.device}, gate_up on {gate_up.device}")
+    if gate_up.n != E * 2 * down.k or down.n != E * H:
+        raise ValueError(f"gate_up [{gate_up.n}, {gate_up.k}] and down [{down.n}, {down.k}] are not {E} stacked "
+                         "experts: expected [E * 2 * ffn, hidden] and [E * hidden, ffn]")
+    for name, t in (("residual", residual), ("out", out)):
+        if t is not None:
+            _check_t(name, t, (M, H), torch.bfloat16, gate_up.device)
+    _check_ws(workspace, gate_up.device)
+    _need_cuda(x, router)
+    with _on(gate_up.device):
+        if out is None:
+            out = torch.empty(M, H, dtype=torch.bfloat16, device=x.device)
+        ids = torch.empty(M, top_k, dtype=torch.int32, device=x.device)
+        weights = torch.empty(M, top_k, dtype=torch.float32, device=x.device)
+        ws = workspace if workspace is not None else _workspace(
+            moe_workspace_bytes(M, E, H, down.k, top_k), x.device)
+        sg, sd = gate_up.struct(), down.struct()
+        _check(lib.nf4_moe_fwd(ctypes.byref(sg), ctypes.byref(sd), _ptr(x), M, _ptr(router), E, int(top_k),
+                               int(bool(renormalise)), _act(act), _ptr(residual), _ptr(out), _ptr(ids),
+                               _ptr(weights), _ptr(ws), ws.numel(), _stream(x.device)), "nf4_moe_fwd")
+    return out, ids, weights
 
 
 def device_status(device=None) -> int:

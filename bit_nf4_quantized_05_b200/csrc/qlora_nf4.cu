@@ -19,6 +19,7 @@
 #include "skinny_tc.cuh"
 #include "decode_stream.cuh"
 #include "merge.cuh"
+#include "moe.cuh"
 
 using namespace nf4;
 
@@ -51,11 +52,13 @@ nf4_status map_fail(int line) {
 // Optional per-kernel event timing (nf4_profiling / nf4_profile_read)
 // ---------------------------------------------------------------------------
 enum KernelKind {
-    KK_QUANTIZE, KK_DEQUANTIZE, KK_LORA_U, KK_LORA_V, KK_LORA_DBDA, KK_ZERO, KK_GEMM_FWD, KK_GEMM_DGRAD, KK_DECODE, KK_DECODE_U, KK_MERGE, KK_LORA_ADD, KK_EPI_BWD, KK_COUNT
+    KK_QUANTIZE, KK_DEQUANTIZE, KK_LORA_U, KK_LORA_V, KK_LORA_DBDA, KK_ZERO, KK_GEMM_FWD, KK_GEMM_DGRAD, KK_DECODE, KK_DECODE_U, KK_MERGE, KK_LORA_ADD, KK_EPI_BWD, KK_MOE_ROUTER, KK_MOE_GATE_UP, KK_MOE_DOWN,
+    KK_COUNT
 };
 const char *const kKindNames[KK_COUNT] = {
     "nf4_quantize", "nf4_dequantize", "lora_u", "lora_v", "lora_dB_dA", "zero_fill", "qlora_gemm_fwd", "qlora_gemm_dgrad", "qlora_decode",
-    "decode_lora_u", "qlora_merge", "lora_dX_add", "epilogue_bwd"};
+    "decode_lora_u", "qlora_merge", "lora_dX_add", "epilogue_bwd", "moe_router", "moe_gate_up",
+    "moe_down"};
 
 struct ProfRecord {
     int kind;
@@ -1386,6 +1389,119 @@ nf4_status qlora_linear_bwd_epilogue(const nf4_weight *w, const uint16_t *x, int
     }
     return bwd_impl(w, x, M, A, B, r, alpha, 0.0f, nullptr, dz, u, dX, dA, dB, workspace, ws_bytes, stream,
                     grads_f32 != 0);
+}
+
+}  // extern "C"
+
+// ---- a mixture of NF4 experts for a few tokens
+
+namespace {
+
+struct MoeLayout {
+    size_t logits, route, done, a, y, total;
+};
+
+MoeLayout moe_layout(int64_t M, int64_t E, int64_t H, int64_t F, int64_t top_k) {
+    MoeLayout L{};
+    size_t off = 0;
+    L.logits = off; off = align256(off + size_t(M) * E * 8);
+    L.route = off;  off = align256(off + sizeof(MoeRoute));
+    L.done = off;   off = align256(off + size_t(H / kMoeRows) * 4);
+    L.a = off;      off = align256(off + size_t(M) * top_k * F * 2);
+    L.y = off;      off = align256(off + size_t(M) * top_k * H * 4);
+    L.total = off;
+    return L;
+}
+
+template <bool DOWN>
+nf4_status launch_moe_experts(const nf4_weight *w, const MoeArgs &base, unsigned grid, cudaStream_t s) {
+    MoeArgs a = base;
+    a.absmax = w->absmax;
+    a.q8 = w->absmax_q8;
+    a.cg = w->absmax_c;
+    a.dq = w->double_quant;
+    a.bshift = block_shift_of(w->block_size);
+    CUtensorMap tm;
+    if (!make_map(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->codes, w->k / 2, w->n, kMoeStepBytes, kMoeRows / 2,
+                  CU_TENSOR_MAP_SWIZZLE_64B))
+        return map_fail(__LINE__);
+    auto kern = nf4_moe_experts_kernel<DOWN>;
+    NF4_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDsDynBytes));
+    LaunchTimer t(DOWN ? KK_MOE_DOWN : KK_MOE_GATE_UP, s);
+    const cudaError_t e = launch_ex(kern, dim3(grid), dim3(kMoeThreads), kDsDynBytes, s, 0u, tm, a);
+    t.stop();
+    if (e != cudaSuccess) return cuda_fail(e, __LINE__);
+    NF4_TRY_CUDA(cudaGetLastError());
+    return NF4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nf4_moe_workspace_bytes(int64_t M, int32_t n_experts, int64_t hidden, int64_t ffn, int32_t top_k) {
+    if (M <= 0 || n_experts <= 0 || hidden <= 0 || ffn <= 0 || top_k <= 0) return 256;
+    return moe_layout(M, n_experts, hidden, ffn, top_k).total;
+}
+
+nf4_status nf4_moe_fwd(const nf4_weight *gate_up, const nf4_weight *down, const uint16_t *x, int64_t M,
+                       const uint16_t *router, int32_t n_experts, int32_t top_k, int32_t renormalise,
+                       int32_t act, const uint16_t *residual, uint16_t *out, int32_t *topk_ids,
+                       float *topk_weights, void *workspace, size_t ws_bytes, void *stream) {
+    nf4_status st = check_weight(gate_up, true);
+    if (st != NF4_OK) return st;
+    st = check_weight(down, true);
+    if (st != NF4_OK) return st;
+    const int64_t E = n_experts, H = gate_up->k, F = down->k;
+    if (M < 0 || M > kMoeMaxTokens || E < 1 || E > kMoeMaxExperts) return NF4_ERR_UNSUPPORTED_SHAPE;
+    if (top_k < 1 || top_k > E || top_k > kMoeMaxTopK) return NF4_ERR_UNSUPPORTED_SHAPE;
+    if (gate_up->n != E * 2 * F || down->n != E * H || H > (1 << 20) || F > (1 << 20)) return NF4_ERR_UNSUPPORTED_SHAPE;
+    if ((renormalise != 0 && renormalise != 1) || act < NF4_ACT_NONE || act > NF4_ACT_GELU) return NF4_ERR_INVALID_ARG;
+    if (M == 0) return NF4_OK;
+    if (!x || !router || !out) return NF4_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(router) || !aligned16(residual) || !aligned16(out) || !aligned16(topk_ids) ||
+        !aligned16(topk_weights))
+        return NF4_ERR_ALIGNMENT;
+    // out is written while residual is still read, an element by the thread
+    // that read it; x is not read any more by then
+    if (residual != out && overlap(residual, out, M * H)) return NF4_ERR_INVALID_ARG;
+    const MoeLayout L = moe_layout(M, E, H, F, top_k);
+    if (!workspace || ws_bytes < L.total) return NF4_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return NF4_ERR_ALIGNMENT;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    MoeArgs a{};
+    a.M = static_cast<int>(M);
+    a.E = n_experts;
+    a.top_k = top_k;
+    a.H = static_cast<int>(H);
+    a.F = static_cast<int>(F);
+    a.act = act;
+    a.renorm = renormalise;
+    a.x = x;
+    a.router = router;
+    a.residual = residual;
+    a.out = out;
+    a.ids = topk_ids;
+    a.weights = topk_weights;
+    a.logits = reinterpret_cast<double *>(ws + L.logits);
+    a.route = reinterpret_cast<MoeRoute *>(ws + L.route);
+    a.a = reinterpret_cast<uint16_t *>(ws + L.a);
+    a.y = reinterpret_cast<float *>(ws + L.y);
+    a.done = reinterpret_cast<int *>(ws + L.done);
+    {
+        LaunchTimer t(KK_MOE_ROUTER, s);
+        const cudaError_t e = launch_ex(nf4_moe_router_kernel,
+                                        dim3(static_cast<unsigned>((E + kMrExperts - 1) / kMrExperts),
+                                             static_cast<unsigned>((M + kMrTokens - 1) / kMrTokens)),
+                                        dim3(kMrThreads), 0, s, 0u, a);
+        t.stop();
+        if (e != cudaSuccess) return cuda_fail(e, __LINE__);
+    }
+    const unsigned grid = static_cast<unsigned>(num_sms(current_device()));
+    st = launch_moe_experts<false>(gate_up, a, grid, s);
+    if (st != NF4_OK) return st;
+    return launch_moe_experts<true>(down, a, grid, s);
 }
 
 }  // extern "C"

@@ -342,6 +342,37 @@ QLORA_API nf4_status qlora_linear_bwd_epilogue(const nf4_weight *w, const uint16
                                                uint16_t *dmul, int32_t grads_f32, void *workspace,
                                                size_t ws_bytes, void *stream);
 
+/* A mixture-of-experts layer over NF4 experts for a few tokens (decoding): each
+ * token goes through the top_k experts its router picks, and only the experts
+ * that some token picked are read.
+ *     l = x R^T,  p = softmax(l) over the n_experts experts
+ *     the top_k largest l (ties: the lower index; NaN counts as -inf), in order,
+ *     with w_j = p_j, or with renormalise == 1 p_j / (sum of the chosen p)
+ *     out = sum_j w_j (act(x Wg^T) . (x Wu^T)) Wd^T  (+ residual)
+ * with Wg, Wu and Wd those of expert j. The experts are stacked: gate_up is
+ * [n_experts * 2 ffn, hidden], for each expert its ffn gate rows and then its ffn
+ * up rows; down is [n_experts * hidden, ffn]; the two may differ in block size and
+ * scale form. x [M, hidden], router [n_experts, hidden], residual (nullable) and
+ * out [M, hidden] bf16; topk_ids [M, top_k] int32 and topk_weights [M, top_k] fp32
+ * (both nullable) receive the routing. Weights enter as in the few-token
+ * form of qlora_linear_fwd (the levels as bf16, each block's fp32 sum times its
+ * scale); the logits are summed in fp64; act(..) . (..) is rounded to bf16; the
+ * weighted sum is fp32, rounded once. out may be the residual itself.
+ * Requirements: 0 <= M <= 64, 1 <= n_experts <= 256, 1 <= top_k <=
+ * min(16, n_experts), hidden and ffn at most 2^20, those of the weights, every
+ * pointer 16-byte aligned. workspace: at least nf4_moe_workspace_bytes(M,
+ * n_experts, hidden, ffn, top_k) bytes, 256-byte aligned; it need not be cleared.
+ * M == 0 is a no-op. No page gives this layer: it is the decoding form of the
+ * linear layer with the weight chosen per token. */
+QLORA_API size_t nf4_moe_workspace_bytes(int64_t M, int32_t n_experts, int64_t hidden, int64_t ffn,
+                                         int32_t top_k);
+QLORA_API nf4_status nf4_moe_fwd(const nf4_weight *gate_up, const nf4_weight *down,
+                                 const uint16_t *x, int64_t M, const uint16_t *router,
+                                 int32_t n_experts, int32_t top_k, int32_t renormalise, int32_t act,
+                                 const uint16_t *residual, uint16_t *out, int32_t *topk_ids,
+                                 float *topk_weights, void *workspace, size_t ws_bytes,
+                                 void *stream);
+
 /* Adapter merge for inference without adapters ("QLoRA explained", section
  * "Merging and deploying"; "How Fine-Tuning LLMs with LoRA and QLoRA Works",
  * FAQ on merging: W_new = W + (alpha/r) B A):
