@@ -16,16 +16,16 @@
 // numbered as slots, expert by expert; the work items are (chunk, 64 weight
 // rows): 32 gate rows and the 32 up rows of the same features, or 64 down rows.
 //
-// An item belongs to a group of 8 warps (two groups a CTA, each with its own
-// barrier, so that one computes while the other joins its sums). The warps
-// split k in steps of 128 elements: warp w takes steps w, w + 8, ... A step is
-// 64 rows x 64 bytes of codes, brought by TMA into the warp's own ring of two
-// slots, one step ahead across items. As in the streaming kernel of the linear
-// layer, a code byte becomes two bf16 levels by one byte permute and one
-// conflict-free shared load, the products run on mma.sync with the tokens as
-// its 8 columns (16 x 8 x 16; a tcgen05 tile would spend 128 rows on at most 8
-// tokens and need the operand written to shared memory), and a 64-element
-// block's fp32 partial is multiplied by its scale once.
+// An item belongs to a group of GW = 4, 8 or 16 warps (16 / GW groups a CTA,
+// each with its own barrier, so that one computes while another joins its
+// sums). The warps split k in steps of 128 elements: warp w takes steps w, w +
+// GW, ... A step is 64 rows x 64 bytes of codes, brought by TMA into the warp's
+// own ring of two slots, one step ahead across items. As in the streaming
+// kernel of the linear layer, a code byte becomes two bf16 levels by one byte
+// permute and one conflict-free shared load, the products run on mma.sync with
+// the tokens as its 8 columns (16 x 8 x 16; a tcgen05 tile would spend 128 rows
+// on at most 8 tokens and need the operand written to shared memory), and a
+// 64-element block's fp32 partial is multiplied by its scale once.
 #pragma once
 
 #include "decode_stream.cuh"
@@ -40,13 +40,20 @@ constexpr int kMoeMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
 constexpr int kMoeChunk = 8;                       // tokens of one work item
 // chunks: every expert's last one may be partly filled
 constexpr int kMoeMaxChunks = kMoeMaxExperts + kMoeMaxSlots / kMoeChunk;
-constexpr int kMoeGroups = 2;
-constexpr int kMoeGroupWarps = 8;
-constexpr int kMoeThreads = 32 * kMoeGroups * kMoeGroupWarps;
+constexpr int kMoeWarps = 16;
+constexpr int kMoeThreads = 32 * kMoeWarps;
 constexpr int kMoeRows = 64;                       // weight rows of one item
 constexpr int kMoeStepBytes = 64;                  // code bytes of one row in a step: 2 blocks
 constexpr int kMoeSlotBytes = kMoeRows * kMoeStepBytes;
 constexpr int kMoeRing = 2;
+
+// The table holds bf16(1.4367 level), and every scale carries the factor that
+// takes it back. bf16 hits some multiples of the 16 levels better than others:
+// over the codes of normally distributed weights the rounding is 0.078% of a
+// weight in the mean square at this factor (found by a search over [1, 2)),
+// against 0.136% for bf16(level) itself.
+constexpr float kMoeLevelUp = 1.4367f;
+constexpr float kMoeLevelDown = 0.69603324f;
 
 struct MoeChunk {
     uint16_t expert;
@@ -154,10 +161,10 @@ nf4_moe_router_kernel(const MoeArgs a) {
 // the space below and above; the header is at the window's start.
 // ---------------------------------------------------------------------------
 struct MoeHeader {
-    uint64_t bars[kMoeGroups * kMoeGroupWarps][kMoeRing];
+    uint64_t bars[kMoeWarps][kMoeRing];
     int abort_flag;
     int nchunks;
-    int last[kMoeGroups];
+    int last[kMoeWarps];                          // by group
     int warp_slots[kMoeMaxExperts / 32], warp_chunks[kMoeMaxExperts / 32];
     MoeChunk chunk[kMoeMaxChunks];
     float weight[kMoeMaxSlots];                   // by slot
@@ -300,27 +307,40 @@ __device__ __forceinline__ void moe_route(const MoeArgs &a, MoeHeader *h) {
     __syncthreads();
 }
 
+template <int THREADS>
 __device__ __forceinline__ void group_sync(int grp) {
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * kMoeGroupWarps) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(THREADS) : "memory");
 }
 
-// One position of a warp in its walk: step kc of work item `item`.
-struct MoePos {
-    int item, kc;
+// A walk over a group's items: (chunk, tile) in steps of the number of groups.
+struct MoeWalk {
+    int chunk, tile;
+    __device__ __forceinline__ void next(int dchunk, int dtile, int tiles) {
+        chunk += dchunk;
+        tile += dtile;
+        if (tile >= tiles) {
+            tile -= tiles;
+            ++chunk;
+        }
+    }
 };
 
-template <bool DOWN>
+// GW: warps of a group. PAIRS: 8-bit scales of 64-element blocks, an even number
+// to a row, so that the two scales of a step are one aligned 16-bit load (the
+// usual weight; the other scale forms take single loads).
+template <bool DOWN, int GW, bool PAIRS>
 __global__ void __launch_bounds__(kMoeThreads, 1)
-nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [rows, K/2] u8, box {64, 32}, 64-byte swizzle
+nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // u8, 64-byte swizzle; down: [rows, K/2], box
+                                                                       // {64, 64}; gate_up: [2 E, F, K/2], box {64, 32, 2}
                        const MoeArgs a) {
+    constexpr int kGroups = kMoeWarps / GW;
     extern __shared__ __align__(1024) uint8_t dsm[];
     const uint32_t sbase = smem_u32(dsm);
     const uint32_t low0 = (sbase + kMoeHeaderBytes + 1023u) & ~1023u;
     const uint32_t win_end = sbase + kDsDynBytes;
     const uint32_t nlow = low0 <= kDsLutAddr ? (kDsLutAddr - low0) / kMoeSlotBytes : 0u;
     const uint32_t nhigh = win_end >= kDsHighAddr ? (win_end - kDsHighAddr) / kMoeSlotBytes : 0u;
-    constexpr uint32_t kSlots = kMoeGroups * kMoeGroupWarps * kMoeRing;
-    if (low0 > kDsLutAddr || win_end < kDsHighAddr || nlow + nhigh < kSlots) {
+    if (low0 > kDsLutAddr || win_end < kDsHighAddr || nlow + nhigh < kMoeWarps * kMoeRing) {
         if (threadIdx.x == 0) record_status(NF4_ERR_CUDA);     // the fixed addresses are not ours
         return;
     }
@@ -328,11 +348,11 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [rows,
     volatile int *abort_flag = &hd->abort_flag;
     uint8_t *lut_g = dsm + (kDsLutAddr - sbase);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int grp = warp / kMoeGroupWarps, gw = warp % kMoeGroupWarps;
+    const int grp = warp / GW, gw = warp % GW;
     const int g = lane >> 2, t = lane & 3;
 
     if (threadIdx.x == 0) {
-        for (int w = 0; w < kMoeGroups * kMoeGroupWarps; ++w)
+        for (int w = 0; w < kMoeWarps; ++w)
             for (int s = 0; s < kMoeRing; ++s) mbar_init(&hd->bars[w][s], 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -340,7 +360,8 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [rows,
     }
     for (int idx = threadIdx.x; idx < 256 * 32; idx += kMoeThreads) {
         const int b = idx >> 5, l = idx & 31;
-        *reinterpret_cast<uint32_t *>(lut_g + b * 256 + 4 * l) = bf16_pack(c_levels[b >> 4], c_levels[b & 15]);
+        *reinterpret_cast<uint32_t *>(lut_g + b * 256 + 4 * l) =
+            bf16_pack(kMoeLevelUp * c_levels[b >> 4], kMoeLevelUp * c_levels[b & 15]);
     }
     griddep_wait();
     griddep_launch_dependents();
@@ -375,32 +396,12 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [rows,
     const int kblocks = K / kBlock;
     const int nkc = (kblocks + 1) / 2;                         // steps of an item
     const int tiles = DOWN ? a.H / kMoeRows : a.F / (kMoeRows / 2);
-    const int nitems = hd->nchunks * tiles;
-    const int stride = static_cast<int>(gridDim.x) * kMoeGroups;
-    const int first = static_cast<int>(blockIdx.x) + grp * static_cast<int>(gridDim.x);
+    const int nchunks = hd->nchunks;
     const int bpr = kblocks >> a.bshift;                       // scale blocks of a weight row
-
-    // first weight row of an item's two 32-row halves
-    auto rows_of = [&](int item, int &r0, int &r1) {
-        const int c = item / tiles, tile = item - c * tiles;
-        const int e = hd->chunk[c].expert;
-        if (DOWN) {
-            r0 = e * a.H + tile * kMoeRows;
-            r1 = r0 + kMoeRows / 2;
-        } else {
-            r0 = e * 2 * a.F + tile * (kMoeRows / 2);
-            r1 = r0 + a.F;
-        }
-    };
-    auto advance = [&](MoePos &p) {
-        p.kc += kMoeGroupWarps;
-        if (p.kc >= nkc) {
-            p.kc = gw;
-            p.item += stride;
-        }
-    };
-    const bool any = gw < nkc;                                 // this warp has steps at all
-    auto valid = [&](const MoePos &p) { return any && p.item < nitems; };
+    const int stride = static_cast<int>(gridDim.x) * kGroups;
+    const int first = static_cast<int>(blockIdx.x) + grp * static_cast<int>(gridDim.x);
+    const int dchunk = stride / tiles, dtile = stride - dchunk * tiles;
+    MoeWalk item{first / tiles, first % tiles};
 
     uint32_t slot[kMoeRing];
 #pragma unroll
@@ -408,125 +409,177 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [rows,
         const uint32_t i = static_cast<uint32_t>(warp * kMoeRing + s);
         slot[s] = i < nlow ? low0 + i * kMoeSlotBytes : kDsHighAddr + (i - nlow) * kMoeSlotBytes;
     }
+
+    // ---- requests: one step ahead of the computation, across items. A warp
+    // with gw >= nkc has no steps and only takes part in the joining of sums.
+    const bool any = gw < nkc;
     int issued = 0, landed = 0;
-    MoePos ip{first, gw};                                      // the next step to request
+    MoeWalk iw = item;
+    int ikc = gw, ic1 = 0, ic2 = 0;                            // box coordinates of iw's item
+    auto box_of = [&]() {
+        if (iw.chunk >= nchunks) return;
+        const int e = hd->chunk[iw.chunk].expert;
+        ic1 = DOWN ? e * a.H + iw.tile * kMoeRows : iw.tile * (kMoeRows / 2);
+        ic2 = 2 * e;
+    };
     auto issue = [&]() {
-        if (!valid(ip) || abort_raised(abort_flag)) return;
+        if (!any || iw.chunk >= nchunks || abort_raised(abort_flag)) return;
         if (lane == 0) {
-            int r0, r1;
-            rows_of(ip.item, r0, r1);
-            uint64_t *bar = &hd->bars[warp][issued % kMoeRing];
-            uint8_t *dst = dsm + (slot[issued % kMoeRing] - sbase);
+            const int s = issued % kMoeRing;
+            uint64_t *bar = &hd->bars[warp][s];
             fence_proxy_async_smem();      // the slot was read through the generic proxy
             mbar_arrive_expect_tx(bar, kMoeSlotBytes);
-            tma_load_2d(dst, &tm_codes, bar, ip.kc * kMoeStepBytes, r0);
-            tma_load_2d(dst + kMoeSlotBytes / 2, &tm_codes, bar, ip.kc * kMoeStepBytes, r1);
+            if constexpr (DOWN) tma_load_2d(dsm + (slot[s] - sbase), &tm_codes, bar, ikc * kMoeStepBytes, ic1);
+            else tma_load_3d(dsm + (slot[s] - sbase), &tm_codes, bar, ikc * kMoeStepBytes, ic1, ic2);
         }
         ++issued;
-        advance(ip);
+        ikc += GW;
+        if (ikc >= nkc) {
+            ikc = gw;
+            iw.next(dchunk, dtile, tiles);
+            box_of();
+        }
     };
 
-    // Raw scales of a step for this lane's two rows: 16 t + prow and 8 more
-    // (the rows whose sums the lane's quad forms in tile t).
     // Which row of a 16-row tile lane group g reads: with 64-byte rows under
     // the 64-byte swizzle, rows {0,1,4,5} (and {2,3,6,7}) of one block take
     // all 32 banks once.
     const int prow = (g & 1) | ((g & 2) << 1) | ((g & 4) >> 1);
-    struct Raw {
-        uint32_t s[2][2];       // [row][block]: q8 code, or the absmax bits
-        float c[2][2];          // their group constants
+
+    // ---- operands of the next step: the raw scales of this lane's two rows
+    // (rows prow and prow + 8 of tile t) and the activations of its token g.
+    // Lanes beyond the chunk's tokens read its last token again: their columns
+    // of the products are never stored. After the group's last item the cursor
+    // stays where it is, so every load below is of something valid.
+    MoeWalk nw = item;
+    int nkc_at = gw;
+    const uint16_t *nx = nullptr;                              // x (or a) at token g, element 16 t
+    uint32_t nsb = 0;                                          // scale index of the first row; the second is 8 bpr on
+    auto operands_of = [&]() {
+        const MoeChunk c = hd->chunk[nw.chunk];
+        const int sl = c.slot0 + min(g, c.n - 1);
+        nx = (DOWN ? a.a + static_cast<int64_t>(sl) * K : a.x + static_cast<int64_t>(hd->token[sl]) * K) + 16 * t;
+        const int row = DOWN ? c.expert * a.H + nw.tile * kMoeRows + 16 * t
+                             : (c.expert * 2 + (t >> 1)) * a.F + nw.tile * (kMoeRows / 2) + 16 * (t & 1);
+        nsb = static_cast<uint32_t>(row + prow) * static_cast<uint32_t>(bpr);
     };
-    auto load_scales = [&](const MoePos &p) -> Raw {
-        Raw r;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                r.s[i][b] = 0u;
-                r.c[i][b] = 0.0f;
+    auto next_operands = [&]() {
+        nkc_at += GW;
+        if (nkc_at >= nkc) {
+            MoeWalk w = nw;
+            w.next(dchunk, dtile, tiles);
+            if (w.chunk < nchunks) {
+                nw = w;
+                nkc_at = gw;
+                operands_of();
+            } else {
+                nkc_at -= GW;
             }
-        if (!valid(p)) return r;
-        int r0, r1;
-        rows_of(p.item, r0, r1);
+        }
+    };
+    uint32_t raw[2][PAIRS ? 1 : 2];                            // [row][block]: q8 codes, or the absmax bits
+    float grp_c[2][PAIRS ? 1 : 2];                             // their group constants
+    auto load_scales = [&]() {
+        const int b0 = 2 * nkc_at;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int row = (t < 2 ? r0 : r1 - kMoeRows / 2) + 16 * t + prow + 8 * i;
-            const int64_t rb = static_cast<int64_t>(row) * bpr;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int blk = 2 * p.kc + b;
-                if (blk < kblocks) {
-                    const int64_t at = rb + (blk >> a.bshift);
-                    if (a.dq) {
-                        r.s[i][b] = __ldg(a.q8 + at);
-                        r.c[i][b] = __ldg(a.cg + (at >> 8));
-                    } else {
-                        r.s[i][b] = __float_as_uint(__ldg(a.absmax + at));
-                    }
+            const uint32_t at = nsb + static_cast<uint32_t>(8 * i * bpr + (b0 >> a.bshift));
+            if constexpr (PAIRS) {
+                raw[i][0] = __ldg(reinterpret_cast<const uint16_t *>(a.q8 + at));
+                grp_c[i][0] = __ldg(a.cg + (at >> 8));
+            } else {
+                // the second block of a step: its own scale, the same one (128-element
+                // blocks), or, behind the row's last block, not used
+                const uint32_t at1 = a.bshift || b0 + 1 >= kblocks ? at : at + 1;
+                if (a.dq) {
+                    raw[i][0] = __ldg(a.q8 + at);
+                    raw[i][1] = __ldg(a.q8 + at1);
+                    grp_c[i][0] = __ldg(a.cg + (at >> 8));
+                    grp_c[i][1] = __ldg(a.cg + (at1 >> 8));
+                } else {
+                    raw[i][0] = __float_as_uint(__ldg(a.absmax + at));
+                    raw[i][1] = __float_as_uint(__ldg(a.absmax + at1));
                 }
             }
         }
-        return r;
     };
-    // the activations of a step: per block the 16 elements [16 t, 16 t + 16) of slot g's token
-    auto load_x = [&](const MoePos &p, uint4 (&xv)[2][2]) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) xv[b][0] = xv[b][1] = make_uint4(0, 0, 0, 0);
-        if (!valid(p)) return;
-        const MoeChunk c = hd->chunk[p.item / tiles];
-        if (g >= c.n) return;
-        const uint16_t *row = DOWN ? a.a + static_cast<int64_t>(c.slot0 + g) * K
-                                   : a.x + static_cast<int64_t>(hd->token[c.slot0 + g]) * K;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int blk = 2 * p.kc + b;
-            if (blk < kblocks) {
-                const uint4 *q = reinterpret_cast<const uint4 *>(row + blk * kBlock + 16 * t);
-                xv[b][0] = q[0];
-                xv[b][1] = q[1];
-            }
+    // (c / 127 by its reciprocal: one rounding away, and the sums are not compared bit for bit)
+    auto scale_of = [&](int i, int b) -> float {
+        if constexpr (PAIRS) {
+            const uint32_t q = b ? raw[i][0] >> 8 : raw[i][0] & 0xffu;
+            return static_cast<float>(q) * (grp_c[i][0] * (kMoeLevelDown / 127.0f));
+        } else {
+            return a.dq ? static_cast<float>(raw[i][b]) * (grp_c[i][b] * (kMoeLevelDown / 127.0f))
+                        : __uint_as_float(raw[i][b]) * kMoeLevelDown;
         }
+    };
+    uint4 xv[2][2];                                            // [block][half]
+    auto load_x = [&](int b) {
+        const int blk = min(2 * nkc_at + b, kblocks - 1);
+        const uint4 *q = reinterpret_cast<const uint4 *>(nx + blk * kBlock);
+        xv[b][0] = q[0];
+        xv[b][1] = q[1];
     };
 
     const uint32_t lanew = (static_cast<uint32_t>(lane) << 2) | (1u << 16);
     const uint32_t swz = static_cast<uint32_t>((prow >> 1) & 3);
     const uint32_t code_row = static_cast<uint32_t>(prow) * kMoeStepBytes + 8u * (t & 1);
     const uint32_t code_chunk[2] = {((0u + (t >> 1)) ^ swz) << 4, ((2u + (t >> 1)) ^ swz) << 4};
+    // this thread's place in the group's partial sums: lane's sums j and j + 8
+    // for j = gw, gw + GW, ... < 8 (j = 4 tile + element)
+    auto park = [&](int w, int j) {
+        return reinterpret_cast<float *>(lut_g + ((grp * GW + w) * 16 + j) * 256 + 128 + 4 * lane);
+    };
 
+    // down: the item before's place in the count of its stripe, looked at one
+    // item later, when the atomic has long returned
+    int seen = -1, seen_tile = 0;
+    auto combine = [&](int tile) {
+        // every slot's share of these 64 columns is there: each token's top_k
+        // of them are added in order
+        const int gt = gw * 32 + lane;
+        const int h = tile * kMoeRows + (gt & 63);
+        for (int m = gt >> 6; m < a.M; m += GW / 2) {
+            float v = 0.0f;
+            for (int j = 0; j < a.top_k; ++j)
+                v += __ldcg(a.y + static_cast<int64_t>(hd->slot_of[m * a.top_k + j]) * a.H + h);
+            const int64_t o = static_cast<int64_t>(m) * a.H + h;
+            if (a.residual) v += bf16_lo(a.residual[o]);
+            const __nv_bfloat16 b = __float2bfloat16_rn(v);
+            a.out[o] = *reinterpret_cast<const uint16_t *>(&b);
+        }
+    };
+
+    box_of();
     issue();
-    MoePos np{first, gw};                                      // the step whose operands are in flight
-    Raw raw = load_scales(np);
-    uint4 xn[2][2];
-    load_x(np, xn);
+    if (any && item.chunk < nchunks) {
+        operands_of();
+        load_scales();
+        load_x(0);
+        load_x(1);
+    }
 
-    for (int item = first; item < nitems; item += stride) {
+    for (; item.chunk < nchunks; item.next(dchunk, dtile, tiles)) {
         float acc[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
-        for (int kc = gw; kc < nkc; kc += kMoeGroupWarps) {
-            uint4 xc[2][2];
+        for (int kc = gw; kc < nkc; kc += GW) {
             float sc[2][2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                xc[b][0] = xn[b][0];
-                xc[b][1] = xn[b][1];
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    // (c / 127 by its reciprocal: one rounding away, and the sums are not compared bit for bit)
-                    sc[i][b] = a.dq ? static_cast<float>(raw.s[i][b]) * (raw.c[i][b] * (1.0f / 127.0f))
-                                    : __uint_as_float(raw.s[i][b]);
-            }
-            advance(np);
-            raw = load_scales(np);
-            load_x(np, xn);
+                for (int i = 0; i < 2; ++i) sc[i][b] = scale_of(i, b);
+            next_operands();
+            load_scales();
             issue();
             const int rs = landed % kMoeRing;
             if (mbar_wait_warp(&hd->bars[warp][rs], static_cast<uint32_t>(landed / kMoeRing) & 1u, abort_flag)) ++landed;
             const uint32_t cbase = slot[rs] + code_row + after_wait_zero();
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
+                if (b == 1 && 2 * kc + 1 >= kblocks) break;    // an odd row's last step is one block
                 uint2 cw[4][2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -536,8 +589,8 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [rows,
                 float pp[4][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const uint4 &xv = xc[b][q >> 1];
-                    const uint32_t b0 = (q & 1) ? xv.z : xv.x, b1 = (q & 1) ? xv.w : xv.y;
+                    const uint4 &x4 = xv[b][q >> 1];
+                    const uint32_t b0 = (q & 1) ? x4.z : x4.x, b1 = (q & 1) ? x4.w : x4.y;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t wl = (q < 2) ? cw[i][0].x : cw[i][0].y;
@@ -558,6 +611,7 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [rows,
                         else mma_bf16_16816(pp[i], af, b0, b1);
                     }
                 }
+                load_x(b);              // the next step's, into the registers just read
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     // rows prow and prow + 8 of tile i: lane (g, i) of this quad has their scales
@@ -569,70 +623,58 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [rows,
                     acc[i][3] = fmaf(s1, pp[i][3], acc[i][3]);
                 }
             }
+            if (2 * kc + 1 >= kblocks) load_x(1);
             __syncwarp();               // every lane has read the slot
         }
 
         // ---- the group's k splits meet in the odd halves of the table rows,
         // and are added in warp order
-        auto park = [&](int w, int j) {
-            return reinterpret_cast<float *>(lut_g + (grp * 128 + w * 16 + j) * 256 + 128 + 4 * lane);
-        };
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) *park(gw, i * 4 + e) = acc[i][e];
-        group_sync(grp);
-        const int ch = item / tiles, tile = item - ch * tiles;
-        const MoeChunk c = hd->chunk[ch];
-        float s0 = 0.0f, s1 = 0.0f;
-        // thread (gw, lane) takes sums gw and gw + 8 of its lane: tile i = j / 4, element e = j % 4
+        if (DOWN && gw == 0 && lane == 0) hd->last[grp] = seen == nchunks - 1;
+        group_sync<32 * GW>(grp);
+        if (DOWN && hd->last[grp]) combine(seen_tile);
+        const MoeChunk c = hd->chunk[item.chunk];
 #pragma unroll
-        for (int w = 0; w < kMoeGroupWarps; ++w) {
-            s0 += *park(w, gw);
-            s1 += *park(w, gw + 8);
-        }
-        const int e = gw & 3, i0 = gw >> 2;
-        const int rr = 16 * i0 + prow + 8 * (e >> 1), col = 2 * t + (e & 1);
-        if constexpr (!DOWN) {
-            // s0 is gate row rr, s1 up row rr
+        for (int j = gw; j < 8; j += GW) {
+            float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < GW; ++w) {
+                s0 += *park(w, j);
+                s1 += *park(w, j + 8);
+            }
+            const int e = j & 3;
+            const int rr = 16 * (j >> 2) + prow + 8 * (e >> 1), col = 2 * t + (e & 1);
             if (col < c.n) {
-                const __nv_bfloat16 v = __float2bfloat16_rn(act_value(s0, a.act) * s1);
-                a.a[static_cast<int64_t>(c.slot0 + col) * a.F + tile * (kMoeRows / 2) + rr] =
-                    *reinterpret_cast<const uint16_t *>(&v);
-            }
-            group_sync(grp);            // the partials are free again
-        } else {
-            const int h0 = tile * kMoeRows;
-            if (col < c.n) {
-                const float w = hd->weight[c.slot0 + col];
-                float *y = a.y + static_cast<int64_t>(c.slot0 + col) * a.H + h0;
-                __stcg(y + rr, w * s0);
-                __stcg(y + rr + 32, w * s1);
-            }
-            __threadfence();
-            group_sync(grp);
-            const int gt = gw * 32 + lane;
-            if (gt == 0) {
-                const int seen = atomicAdd(a.done + tile, 1);
-                __threadfence();
-                hd->last[grp] = seen == hd->nchunks - 1;
-            }
-            group_sync(grp);
-            if (hd->last[grp]) {
-                // every slot's share of these 64 columns is there: each token's
-                // top_k of them are added in order
-                const int h = h0 + (gt & 63);
-                for (int m = gt >> 6; m < a.M; m += 4) {
-                    float v = 0.0f;
-                    for (int j = 0; j < a.top_k; ++j)
-                        v += __ldcg(a.y + static_cast<int64_t>(hd->slot_of[m * a.top_k + j]) * a.H + h);
-                    const int64_t o = static_cast<int64_t>(m) * a.H + h;
-                    if (a.residual) v += bf16_lo(a.residual[o]);
-                    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-                    a.out[o] = *reinterpret_cast<const uint16_t *>(&b);
+                if constexpr (!DOWN) {
+                    // s0 is gate row rr, s1 up row rr
+                    const __nv_bfloat16 v = __float2bfloat16_rn(act_value(s0, a.act) * s1);
+                    a.a[static_cast<int64_t>(c.slot0 + col) * a.F + item.tile * (kMoeRows / 2) + rr] =
+                        *reinterpret_cast<const uint16_t *>(&v);
+                } else {
+                    const float w = hd->weight[c.slot0 + col];
+                    float *y = a.y + static_cast<int64_t>(c.slot0 + col) * a.H + item.tile * kMoeRows + rr;
+                    __stcg(y, w * s0);
+                    __stcg(y + 32, w * s1);
                 }
             }
         }
+        group_sync<32 * GW>(grp);        // the partials are free again, the products written
+        if (DOWN) {
+            seen_tile = item.tile;
+            if (gw == 0 && lane == 0) {
+                __threadfence();         // the group's products before the count
+                seen = atomicAdd(a.done + item.tile, 1);
+                __threadfence();
+            }
+        }
+    }
+    if (DOWN) {
+        if (gw == 0 && lane == 0) hd->last[grp] = seen == nchunks - 1;
+        group_sync<32 * GW>(grp);
+        if (hd->last[grp]) combine(seen_tile);
     }
     // leave no copy in flight into shared memory that is about to be released
     // (after a normal end every copy has landed)

@@ -1413,8 +1413,39 @@ MoeLayout moe_layout(int64_t M, int64_t E, int64_t H, int64_t F, int64_t top_k) 
     return L;
 }
 
+// 3-D row-major tensor [outer, mid, inner] of bytes.
+bool make_map_3d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t mid, uint64_t outer, uint32_t box_inner,
+                 uint32_t box_mid, uint32_t box_outer, CUtensorMapSwizzle sw) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {inner, mid, outer};
+    cuuint64_t strides[2] = {inner, inner * mid};
+    cuuint32_t box[3] = {box_inner, box_mid, box_outer};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Warps of a group: the choice with the smallest (rounds of items over the
+// groups) x (steps of a warp per item + 1), the 1 standing for what an item
+// costs beside its steps.
+int pick_moe_group(int64_t items, int64_t steps, int sms) {
+    int best = 4;
+    int64_t best_cost = -1;
+    for (int gw : {4, 8, 16}) {
+        const int64_t groups = int64_t(sms) * (kMoeWarps / gw);
+        const int64_t cost = ((items + groups - 1) / groups) * ((steps + gw - 1) / gw + 1);
+        if (best_cost < 0 || cost < best_cost) {
+            best = gw;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
 template <bool DOWN>
-nf4_status launch_moe_experts(const nf4_weight *w, const MoeArgs &base, unsigned grid, cudaStream_t s) {
+nf4_status launch_moe_experts(const nf4_weight *w, const MoeArgs &base, cudaStream_t s) {
     MoeArgs a = base;
     a.absmax = w->absmax;
     a.q8 = w->absmax_q8;
@@ -1422,13 +1453,34 @@ nf4_status launch_moe_experts(const nf4_weight *w, const MoeArgs &base, unsigned
     a.dq = w->double_quant;
     a.bshift = block_shift_of(w->block_size);
     CUtensorMap tm;
-    if (!make_map(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->codes, w->k / 2, w->n, kMoeStepBytes, kMoeRows / 2,
-                  CU_TENSOR_MAP_SWIZZLE_64B))
-        return map_fail(__LINE__);
-    auto kern = nf4_moe_experts_kernel<DOWN>;
+    const bool ok = DOWN ? make_map(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->codes, w->k / 2, w->n, kMoeStepBytes,
+                                    kMoeRows, CU_TENSOR_MAP_SWIZZLE_64B)
+                         : make_map_3d(&tm, w->codes, w->k / 2, a.F, 2 * a.E, kMoeStepBytes, kMoeRows / 2, 2,
+                                       CU_TENSOR_MAP_SWIZZLE_64B);
+    if (!ok) return map_fail(__LINE__);
+    // chunks: at least one per chosen expert; how many experts that is, only
+    // the device knows, so the rule takes the expected number of a router
+    // that spreads its tokens evenly
+    const int sms = num_sms(current_device());
+    const double idle = std::pow(1.0 - double(a.top_k) / a.E, double(a.M));
+    const int64_t chunks = std::max<int64_t>(1, std::llround(a.E * (1.0 - idle)));
+    const int64_t tiles = DOWN ? a.H / kMoeRows : a.F / (kMoeRows / 2);
+    const int64_t steps = (w->k / kBlock + 1) / 2;
+    const int gw = pick_moe_group(chunks * tiles, steps, sms);
+    const bool pairs = w->double_quant && w->block_size == 64 && w->k / kBlock % 2 == 0;
+    auto kern = nf4_moe_experts_kernel<DOWN, 4, true>;
+#define NF4_MOE_CASE(GW_, PAIRS_) \
+    if (gw == GW_ && pairs == PAIRS_) kern = nf4_moe_experts_kernel<DOWN, GW_, PAIRS_>;
+    NF4_MOE_CASE(8, true)
+    NF4_MOE_CASE(16, true)
+    NF4_MOE_CASE(4, false)
+    NF4_MOE_CASE(8, false)
+    NF4_MOE_CASE(16, false)
+#undef NF4_MOE_CASE
     NF4_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDsDynBytes));
     LaunchTimer t(DOWN ? KK_MOE_DOWN : KK_MOE_GATE_UP, s);
-    const cudaError_t e = launch_ex(kern, dim3(grid), dim3(kMoeThreads), kDsDynBytes, s, 0u, tm, a);
+    const cudaError_t e =
+        launch_ex(kern, dim3(static_cast<unsigned>(sms)), dim3(kMoeThreads), kDsDynBytes, s, 0u, tm, a);
     t.stop();
     if (e != cudaSuccess) return cuda_fail(e, __LINE__);
     NF4_TRY_CUDA(cudaGetLastError());
@@ -1456,6 +1508,8 @@ nf4_status nf4_moe_fwd(const nf4_weight *gate_up, const nf4_weight *down, const 
     if (M < 0 || M > kMoeMaxTokens || E < 1 || E > kMoeMaxExperts) return NF4_ERR_UNSUPPORTED_SHAPE;
     if (top_k < 1 || top_k > E || top_k > kMoeMaxTopK) return NF4_ERR_UNSUPPORTED_SHAPE;
     if (gate_up->n != E * 2 * F || down->n != E * H || H > (1 << 20) || F > (1 << 20)) return NF4_ERR_UNSUPPORTED_SHAPE;
+    if (gate_up->n * (H / kBlock) >= (int64_t(1) << 32) || down->n * (F / kBlock) >= (int64_t(1) << 32))
+        return NF4_ERR_UNSUPPORTED_SHAPE;      // 32-bit block indices
     if ((renormalise != 0 && renormalise != 1) || act < NF4_ACT_NONE || act > NF4_ACT_GELU) return NF4_ERR_INVALID_ARG;
     if (M == 0) return NF4_OK;
     if (!x || !router || !out) return NF4_ERR_INVALID_ARG;
@@ -1498,10 +1552,9 @@ nf4_status nf4_moe_fwd(const nf4_weight *gate_up, const nf4_weight *down, const 
         t.stop();
         if (e != cudaSuccess) return cuda_fail(e, __LINE__);
     }
-    const unsigned grid = static_cast<unsigned>(num_sms(current_device()));
-    st = launch_moe_experts<false>(gate_up, a, grid, s);
+    st = launch_moe_experts<false>(gate_up, a, s);
     if (st != NF4_OK) return st;
-    return launch_moe_experts<true>(down, a, grid, s);
+    return launch_moe_experts<true>(down, a, s);
 }
 
 }  // extern "C"

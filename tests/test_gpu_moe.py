@@ -1,7 +1,7 @@
 """The mixture of NF4 experts for a few tokens against its definition in 64 bits.
 
-The oracle takes the weight as the kernel's products do: the level rounded to
-bf16 times the fp32 block scale. Left are the rounding of act(gate) . up to
+The oracle takes the weight as the kernel's products do: a multiple of the level
+rounded to bf16, times the fp32 block scale over that multiple. Left are the rounding of act(gate) . up to
 bf16, fp32 sums, and the output's rounding; the bound follows them through."""
 import pytest
 import torch
@@ -20,9 +20,9 @@ def q():
 
 
 def operand(qw, rows):
-    """bf16(level) * scale of some rows, in 64 bits, on the GPU."""
+    """bf16(1.4367 level) * 0.69603324 scale of some rows, in 64 bits, on the GPU."""
     from perf.operators import LEVELS
-    lv = torch.tensor(LEVELS).bfloat16().double().cuda()
+    lv = (torch.tensor(LEVELS) * 1.4367).bfloat16().double().cuda() * 0.69603324
     c = qw.codes.view(qw.n, qw.k // 2)[rows]
     codes = torch.stack((c >> 4, c & 15), -1).view(c.shape[0], qw.k)
     nb = qw.n * qw.k // qw.block_size
