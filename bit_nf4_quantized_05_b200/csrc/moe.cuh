@@ -3,11 +3,11 @@
 //   l = x R^T, p = softmax(l), the top_k experts of each token with weights w
 //   a_e = act(x Wg_e^T) . (x Wu_e^T),   out = sum_j w_j a_{e_j} Wd_{e_j}^T (+ residual)
 //
-// Three kernels, each launched while the one before it drains:
-//   nf4_moe_router_kernel         the logits, summed in fp64
-//   nf4_moe_experts_kernel<false> routing (every CTA for itself: the logits are
-//                                 a few KB), then a_e of the chosen experts
-//   nf4_moe_experts_kernel<true>  the down products, their weighted sum
+// Two kernels, the second launched while the first drains:
+//   nf4_moe_router_kernel    the logits, summed in fp64
+//   nf4_moe_experts_kernel   routing (every CTA for itself: the logits are a few
+//                            KB), a_e of the chosen experts, then the down
+//                            products and their weighted sum
 // The experts' codes are nearly all the bytes: 3 H F / 2 per chosen expert.
 //
 // A token chooses an expert at most once, so routing is a bit mask of tokens
@@ -15,6 +15,12 @@
 // expert's tokens are cut into chunks of 8 (the columns of one MMA) and
 // numbered as slots, expert by expert; the work items are (chunk, 64 weight
 // rows): 32 gate rows and the 32 up rows of the same features, or 64 down rows.
+// Groups of warps take items from one counter, all gate-up items before the
+// down items. A down item waits until its chunk's gate-up items are done; those
+// were all taken before it by groups that are running and never wait, so the
+// wait ends whatever part of the grid is resident. (As two kernels, the second
+// one's start and the first one's last, uneven round cost 12 of 105 us for 16
+// tokens at 6 of 64 experts of 2048 x 1408.)
 //
 // An item belongs to a group of GW = 4, 8 or 16 warps (16 / GW groups a CTA,
 // each with its own barrier, so that one computes while another joins its
@@ -27,6 +33,9 @@
 // on at most 8 tokens and need the operand written to shared memory), and a
 // 64-element block's fp32 partial is multiplied by its scale once.
 #pragma once
+
+#include <cstddef>
+#include <type_traits>
 
 #include "decode_stream.cuh"
 #include "epilogue.cuh"
@@ -62,13 +71,20 @@ struct MoeChunk {
     uint16_t pad;
 };
 
-// What routing leaves in the workspace for the down kernel.
-struct MoeRoute {
-    int nchunks;
-    int pad[3];
-    MoeChunk chunk[kMoeMaxChunks];
-    float weight[kMoeMaxSlots];           // by slot
-    uint16_t slot_of[kMoeMaxSlots];       // by token * top_k + j
+// Scales of one of the two expert weights.
+struct MoeScales {
+    const float *absmax;
+    const uint8_t *q8;
+    const float *cg;
+    int dq, bshift;
+};
+
+// Counters of one call in the workspace, cleared by the router kernel.
+struct MoeCounters {
+    int claimed;                  // work items taken
+    int gate_up_done;             // gate-up items finished
+    int chunk_done[kMoeMaxChunks];    // by chunk
+    int stripe_done[1];           // [H / 64] down items finished of each stripe of out
 };
 
 struct MoeArgs {
@@ -80,77 +96,102 @@ struct MoeArgs {
     uint16_t *out;                // [M, H]
     int32_t *ids;                 // [M, top_k] or null
     float *weights;               // [M, top_k] or null
-    // scales of the expert weight of this launch (gate_up or down)
-    const float *absmax;
-    const uint8_t *q8;
-    const float *cg;
-    int dq, bshift;
+    MoeScales gate_up, down;
     // workspace
-    double *logits;               // [M, E]
-    MoeRoute *route;
+    int splits;                   // of H in the router kernel
+    double *logits;               // [splits, M, E] partial sums
+    MoeCounters *cnt;
     uint16_t *a;                  // [slots, F] bf16
     float *y;                     // [slots, H] weighted down products
-    int *done;                    // [H / 64] items finished of each stripe of out
 };
 
 // ---------------------------------------------------------------------------
 // Router logits in fp64: which experts a token takes is decided by comparing
 // them, and a product of two bf16 values is exact in fp64, so sums that differ
-// only in their order practically never swap two experts. A CTA forms 4 tokens
-// x 4 experts, its 8 warps splitting H.
+// only in their order practically never swap two experts. Bound by latency: a
+// CTA forms 4 tokens x 4 experts over 1024 elements of H, 8 to a thread, so that
+// every load is in flight at once, and the routing adds the splits in order.
+// bf16 becomes fp64 by moving bits: the conversion instruction runs at a few
+// results a clock and took 13 of this kernel's 15 us at H = 5120.
 // ---------------------------------------------------------------------------
-constexpr int kMrThreads = 256;
+constexpr int kMrThreads = 128;
+constexpr int kMrSplit = kMrThreads * 8;
 constexpr int kMrTokens = 4, kMrExperts = 4;
 
+// The fp64 value of the bf16 in the low half of b.
+__device__ __forceinline__ double bf16_to_f64(uint32_t b) {
+    const uint32_t mag = b & 0x7fffu, sign = (b & 0x8000u) << 16;
+    if (mag < 0x80u)                                   // zero, or below the normal range
+        return mag ? static_cast<double>(__uint_as_float(b << 16)) : __hiloint2double(static_cast<int>(sign), 0);
+    // exponent bias 1023 for 127; all ones (infinity, NaN) stays all ones
+    const uint32_t hi = (mag << 13) + (mag >= 0x7f80u ? 2u * (896u << 20) : 896u << 20);
+    return __hiloint2double(static_cast<int>(hi | sign), 0);
+}
+
 __device__ __forceinline__ void bf16_to_f64(const uint4 &v, double (&d)[8]) {
-    float f[8];
-    bf16_unpack8(v, f);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] = static_cast<double>(f[i]);
+    for (int i = 0; i < 4; ++i) {
+        d[2 * i] = bf16_to_f64(w[i] & 0xffffu);
+        d[2 * i + 1] = bf16_to_f64(w[i] >> 16);
+    }
 }
 
 __global__ void __launch_bounds__(kMrThreads)
 nf4_moe_router_kernel(const MoeArgs a) {
-    __shared__ double part[kMrThreads / 32][kMrTokens * kMrExperts];
+    constexpr int kOut = kMrTokens * kMrExperts;
+    __shared__ double part[kMrThreads / 32][kOut];
     griddep_wait();
     griddep_launch_dependents();
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int i = threadIdx.x; i < a.H / kMoeRows; i += kMrThreads) a.done[i] = 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+        int *c = reinterpret_cast<int *>(a.cnt);
+        const int n = static_cast<int>(offsetof(MoeCounters, stripe_done) / 4) + a.H / kMoeRows;
+        for (int i = threadIdx.x; i < n; i += kMrThreads) c[i] = 0;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e0 = static_cast<int>(blockIdx.x) * kMrExperts, m0 = static_cast<int>(blockIdx.y) * kMrTokens;
-    double acc[kMrTokens][kMrExperts] = {};
-    for (int k = threadIdx.x * 8; k < a.H; k += kMrThreads * 8) {
+    const int k = static_cast<int>(blockIdx.z) * kMrSplit + threadIdx.x * 8;
+    double acc[kOut] = {};                             // [token][expert]
+    if (k < a.H) {
+        uint4 wv[kMrExperts], xv[kMrTokens];
+#pragma unroll
+        for (int j = 0; j < kMrExperts; ++j)           // rows behind the last are read as the last
+            wv[j] = __ldg(reinterpret_cast<const uint4 *>(a.router + static_cast<int64_t>(min(e0 + j, a.E - 1)) * a.H + k));
+#pragma unroll
+        for (int i = 0; i < kMrTokens; ++i)
+            xv[i] = *reinterpret_cast<const uint4 *>(a.x + static_cast<int64_t>(min(m0 + i, a.M - 1)) * a.H + k);
         double w[kMrExperts][8];
 #pragma unroll
-        for (int j = 0; j < kMrExperts; ++j)
-            if (e0 + j < a.E)
-                bf16_to_f64(__ldg(reinterpret_cast<const uint4 *>(a.router + static_cast<int64_t>(e0 + j) * a.H + k)), w[j]);
+        for (int j = 0; j < kMrExperts; ++j) bf16_to_f64(wv[j], w[j]);
 #pragma unroll
         for (int i = 0; i < kMrTokens; ++i) {
             if (m0 + i >= a.M) break;
             double x[8];
-            bf16_to_f64(*reinterpret_cast<const uint4 *>(a.x + static_cast<int64_t>(m0 + i) * a.H + k), x);
+            bf16_to_f64(xv[i], x);
 #pragma unroll
             for (int j = 0; j < kMrExperts; ++j)
-                if (e0 + j < a.E)
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) acc[i][j] = fma(x[c], w[j][c], acc[i][j]);
+                for (int c = 0; c < 8; ++c) acc[i * kMrExperts + j] = fma(x[c], w[j][c], acc[i * kMrExperts + j]);
         }
     }
+    // sums over the warp: each step halves the sums a lane still holds; after
+    // four, lane l has sum (l >> 1) of its pair
 #pragma unroll
-    for (int i = 0; i < kMrTokens; ++i)
+    for (int h = kOut / 2, o = 16; h >= 1; h >>= 1, o >>= 1)
 #pragma unroll
-        for (int j = 0; j < kMrExperts; ++j) {
-            double v = acc[i][j];
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0) part[warp][i * kMrExperts + j] = v;
+        for (int i = 0; i < h; ++i) {
+            const bool up = (lane & o) != 0;
+            const double keep = up ? acc[i + h] : acc[i], send = up ? acc[i] : acc[i + h];
+            acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
+    acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
+    if (!(lane & 1)) part[warp][lane >> 1] = acc[0];
     __syncthreads();
-    if (threadIdx.x < kMrTokens * kMrExperts) {
+    if (threadIdx.x < kOut) {
         const int m = m0 + threadIdx.x / kMrExperts, e = e0 + threadIdx.x % kMrExperts;
         double v = 0.0;
         for (int w = 0; w < kMrThreads / 32; ++w) v += part[w][threadIdx.x];
-        if (m < a.M && e < a.E) a.logits[static_cast<int64_t>(m) * a.E + e] = v;
+        if (m < a.M && e < a.E) a.logits[(static_cast<int64_t>(blockIdx.z) * a.M + m) * a.E + e] = v;
     }
 }
 
@@ -164,18 +205,15 @@ struct MoeHeader {
     uint64_t bars[kMoeWarps][kMoeRing];
     int abort_flag;
     int nchunks;
-    int last[kMoeWarps];                          // by group
+    int last[kMoeWarps], ready[kMoeWarps];        // by group
+    uint32_t claim[kMoeWarps][4];                 // by group: its items, a ring of four
     int warp_slots[kMoeMaxExperts / 32], warp_chunks[kMoeMaxExperts / 32];
     MoeChunk chunk[kMoeMaxChunks];
     float weight[kMoeMaxSlots];                   // by slot
     uint16_t slot_of[kMoeMaxSlots];               // by token * top_k + j
-    union {
-        struct {                                  // while routing
-            unsigned long long mask[kMoeMaxExperts];   // tokens of each expert
-            float w[kMoeMaxSlots];                     // by token * top_k + j
-            uint8_t id[kMoeMaxSlots];
-        };
-    };
+    unsigned long long mask[kMoeMaxExperts];      // tokens of each expert
+    float w[kMoeMaxSlots];                        // by token * top_k + j
+    uint8_t id[kMoeMaxSlots];
     uint8_t token[kMoeMaxSlots];                  // by slot
     uint16_t slot0[kMoeMaxExperts];
 };
@@ -183,75 +221,86 @@ static_assert(kMoeMaxExperts <= 256 && kMoeMaxTokens <= 64, "ids in a byte, toke
 constexpr int kMoeHeaderBytes = (sizeof(MoeHeader) + 1023) / 1024 * 1024;
 static_assert(kMoeHeaderBytes <= 20 * 1024, "header");
 
+// fp64 values as integers of the same order, from 1 on: NaN is 1, below the rest.
+__device__ __forceinline__ unsigned long long order_key(double v) {
+    const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v));
+    return isnan(v) ? 1ull : (b >> 63 ? ~b : b | 1ull << 63) + 1ull;
+}
+__device__ __forceinline__ double key_value(unsigned long long key) {
+    const unsigned long long b = key - 1ull;
+    return __longlong_as_double(static_cast<long long>(b >> 63 ? b & ~(1ull << 63) : ~b));
+}
+
+// The largest key of the warp.
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long key) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32) == hi ? static_cast<uint32_t>(key) : 0u);
+    return static_cast<unsigned long long>(hi) << 32 | lo;
+}
+
 // Routing of all tokens, by every thread of the CTA: the chosen experts with
 // their weights, the chunks, and the slots. Larger logit first, ties to the
 // lower index; a NaN counts as minus infinity (its weights are NaN all the same).
-__device__ __forceinline__ void moe_route(const MoeArgs &a, MoeHeader *h) {
+// A warp takes a token, with the experts' keys in the odd halves of 16 table
+// rows. The loops stay rolled: this runs once a launch, and fetching the
+// instructions of an unrolled form took most of its 4 us.
+__device__ __forceinline__ void moe_route(const MoeArgs &a, MoeHeader *h, uint8_t *table) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const double ninf = -INFINITY;
     for (int e = threadIdx.x; e < kMoeMaxExperts; e += kMoeThreads) h->mask[e] = 0;
     __syncthreads();
+    // expert e's key; 0 once it is taken
+    auto key = [&](int e) -> unsigned long long & {
+        return *reinterpret_cast<unsigned long long *>(table + (warp * 16 + (e >> 4)) * 256 + 128 + (e & 15) * 8);
+    };
+    const int64_t split = static_cast<int64_t>(a.M) * a.E;
+#pragma unroll 1
     for (int m = warp; m < a.M; m += kMoeThreads / 32) {
-        constexpr int kPer = kMoeMaxExperts / 32;
-        double v[kPer];
-        float ex[kPer];
-        double top = ninf;
         bool nan = false;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = lane + 32 * i;
-            v[i] = e < a.E ? __ldcg(a.logits + static_cast<int64_t>(m) * a.E + e) : ninf;
-            if (isnan(v[i])) {
-                nan = true;
-                v[i] = ninf;
-            }
-            top = fmax(top, v[i]);
+        unsigned long long best = 0;
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32) {
+            const double *l = a.logits + static_cast<int64_t>(m) * a.E + e;
+            double v = 0.0;
+#pragma unroll 4
+            for (int s = 0; s < a.splits; ++s) v += __ldcg(l + s * split);
+            nan |= isnan(v);
+            key(e) = order_key(v);
+            best = max(best, key(e));
         }
-        for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
         nan = __any_sync(0xffffffffu, nan) != 0;
+        const double top = key_value(warp_max(best));
+        // (infinities propagate through the sum as in a softmax)
         float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            ex[i] = lane + 32 * i < a.E ? expf(static_cast<float>(v[i] - top)) : 0.0f;
-            sum += ex[i];
+        if (!a.renorm) {
+#pragma unroll 1
+            for (int e = lane; e < a.E; e += 32) sum += expf(static_cast<float>(key_value(key(e)) - top));
         }
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        float chosen = 0.0f, mine = 0.0f;
-        uint32_t taken = 0;                      // of this lane's experts
+        double mine = top;
         int my_id = 0;
+#pragma unroll 1
         for (int j = 0; j < a.top_k; ++j) {
-            double b = ninf;
-            int bi = 0x7fffffff;
-            float be = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int e = lane + 32 * i;
-                if (e < a.E && !((taken >> i) & 1u) && (bi == 0x7fffffff || v[i] > b)) {
-                    b = v[i];
+            unsigned long long b = 0;
+            int bi = 0;
+#pragma unroll 1
+            for (int e = lane; e < a.E; e += 32)
+                if (key(e) > b) {
+                    b = key(e);
                     bi = e;
-                    be = ex[i];
                 }
-            }
-            for (int o = 16; o > 0; o >>= 1) {
-                const double ob = __shfl_xor_sync(0xffffffffu, b, o);
-                const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-                const float oe = __shfl_xor_sync(0xffffffffu, be, o);
-                if (ob > b || (ob == b && oi < bi)) {
-                    b = ob;
-                    bi = oi;
-                    be = oe;
-                }
-            }
-            if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
-            chosen += be;
+            const unsigned long long m1 = warp_max(b);
+            const int win = static_cast<int>(__reduce_min_sync(0xffffffffu, b == m1 ? static_cast<uint32_t>(bi) : 0xffffu));
+            if ((win & 31) == lane) key(win) = 0;
             if (lane == j) {
-                my_id = bi;
-                mine = be;
+                my_id = win;
+                mine = key_value(m1);
             }
         }
+        const float ex = lane < a.top_k ? expf(static_cast<float>(mine - top)) : 0.0f;
+        if (a.renorm) sum = ex;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane < a.top_k) {
-            float w = mine / (a.renorm ? chosen : sum);
-            if (nan) w = __int_as_float(0x7fffffff);
+            const float w = nan ? __int_as_float(0x7fffffff) : ex / sum;
             const int i = m * a.top_k + lane;
             h->id[i] = static_cast<uint8_t>(my_id);
             h->w[i] = w;
@@ -261,6 +310,7 @@ __device__ __forceinline__ void moe_route(const MoeArgs &a, MoeHeader *h) {
                 if (a.weights) a.weights[i] = w;
             }
         }
+        __syncwarp();
     }
     __syncthreads();
     // exclusive sums over the experts of their slots and chunks
@@ -271,6 +321,7 @@ __device__ __forceinline__ void moe_route(const MoeArgs &a, MoeHeader *h) {
         nc = (n + kMoeChunk - 1) / kMoeChunk;
         s_in = n;
         c_in = nc;
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int s = __shfl_up_sync(0xffffffffu, s_in, o), c = __shfl_up_sync(0xffffffffu, c_in, o);
             if (lane >= o) {
@@ -304,7 +355,6 @@ __device__ __forceinline__ void moe_route(const MoeArgs &a, MoeHeader *h) {
         h->slot_of[i] = static_cast<uint16_t>(s);
         h->weight[s] = h->w[i];
     }
-    __syncthreads();
 }
 
 template <int THREADS>
@@ -312,28 +362,27 @@ __device__ __forceinline__ void group_sync(int grp) {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(THREADS) : "memory");
 }
 
-// A walk over a group's items: (chunk, tile) in steps of the number of groups.
-struct MoeWalk {
-    int chunk, tile;
-    __device__ __forceinline__ void next(int dchunk, int dtile, int tiles) {
-        chunk += dchunk;
-        tile += dtile;
-        if (tile >= tiles) {
-            tile -= tiles;
-            ++chunk;
-        }
-    }
-};
+// A work item as one word: down (bit 31), chunk (bits 22..30), tile (bits 0..21).
+constexpr uint32_t kMoeNoItem = 0xffffffffu;
+__device__ __forceinline__ int item_chunk(uint32_t it) { return static_cast<int>((it >> 22) & 511u); }
+__device__ __forceinline__ int item_tile(uint32_t it) { return static_cast<int>(it & 0x3fffffu); }
+__device__ __forceinline__ bool item_down(uint32_t it) { return (it >> 31) != 0; }
+static_assert(kMoeMaxChunks < 511, "chunk field, with the empty item apart");
+
+__device__ __forceinline__ int load_acquire_gpu(const int *p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 
 // GW: warps of a group. PAIRS: 8-bit scales of 64-element blocks, an even number
 // to a row, so that the two scales of a step are one aligned 16-bit load (the
 // usual weight; the other scale forms take single loads).
-template <bool DOWN, int GW, bool PAIRS>
+template <int GW, bool PAIRS>
 __global__ void __launch_bounds__(kMoeThreads, 1)
-nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // u8, 64-byte swizzle; down: [rows, K/2], box
-                                                                       // {64, 64}; gate_up: [2 E, F, K/2], box {64, 32, 2}
+nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate_up,   // u8 [2 E, F, H/2], box {64, 32, 2}, 64-byte swizzle
+                       const __grid_constant__ CUtensorMap tm_down,      // u8 [E H, F/2], box {64, 64}, 64-byte swizzle
                        const MoeArgs a) {
-    constexpr int kGroups = kMoeWarps / GW;
     extern __shared__ __align__(1024) uint8_t dsm[];
     const uint32_t sbase = smem_u32(dsm);
     const uint32_t low0 = (sbase + kMoeHeaderBytes + 1023u) & ~1023u;
@@ -356,7 +405,8 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // u8, 64
             for (int s = 0; s < kMoeRing; ++s) mbar_init(&hd->bars[w][s], 1);
         *abort_flag = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&tm_codes);
+        tma_prefetch_desc(&tm_gate_up);
+        tma_prefetch_desc(&tm_down);
     }
     for (int idx = threadIdx.x; idx < 256 * 32; idx += kMoeThreads) {
         const int b = idx >> 5, l = idx & 31;
@@ -365,43 +415,34 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // u8, 64
     }
     griddep_wait();
     griddep_launch_dependents();
-    if constexpr (!DOWN) {
-        __syncthreads();
-        moe_route(a, hd);
-        if (blockIdx.x == 0) {
-            MoeRoute *r = a.route;
-            if (threadIdx.x == 0) r->nchunks = hd->nchunks;
-            for (int i = threadIdx.x; i < hd->nchunks; i += kMoeThreads) r->chunk[i] = hd->chunk[i];
-            for (int i = threadIdx.x; i < a.M * a.top_k; i += kMoeThreads) {
-                r->weight[i] = hd->weight[i];
-                r->slot_of[i] = hd->slot_of[i];
-            }
-        }
-    } else {
-        const MoeRoute *r = a.route;
-        const int most = min(kMoeMaxChunks, a.M * a.top_k);
-        if (threadIdx.x == 0) hd->nchunks = __ldcg(&r->nchunks);
-        for (int i = threadIdx.x; i < most; i += kMoeThreads) {
-            const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(r->chunk) + i);
-            *reinterpret_cast<uint2 *>(&hd->chunk[i]) = v;
-        }
-        for (int i = threadIdx.x; i < a.M * a.top_k; i += kMoeThreads) {
-            hd->weight[i] = __ldcg(r->weight + i);
-            hd->slot_of[i] = __ldcg(r->slot_of + i);
-        }
-        __syncthreads();
-    }
 
-    const int K = DOWN ? a.F : a.H;
-    const int kblocks = K / kBlock;
-    const int nkc = (kblocks + 1) / 2;                         // steps of an item
-    const int tiles = DOWN ? a.H / kMoeRows : a.F / (kMoeRows / 2);
+    // ---- items are taken by the group's first thread, two ahead of the one
+    // being computed: the last step of an item already requests the next one's
+    // data, and the atomic of the one after it is in flight meanwhile. At the
+    // start a group takes one at a time, so that few items spread over the grid.
+    const bool taker = gw == 0 && lane == 0;
+    int taken = 0;
+    if (taker) taken = atomicAdd(&a.cnt->claimed, 1);
+    moe_route(a, hd, lut_g);
+    __syncthreads();
     const int nchunks = hd->nchunks;
-    const int bpr = kblocks >> a.bshift;                       // scale blocks of a weight row
-    const int stride = static_cast<int>(gridDim.x) * kGroups;
-    const int first = static_cast<int>(blockIdx.x) + grp * static_cast<int>(gridDim.x);
-    const int dchunk = stride / tiles, dtile = stride - dchunk * tiles;
-    MoeWalk item{first / tiles, first % tiles};
+    const int tiles_gu = a.F / (kMoeRows / 2), tiles_dn = a.H / kMoeRows;
+    const int items_gu = nchunks * tiles_gu;
+    auto item_of = [&](int i) -> uint32_t {
+        const bool dn = i >= items_gu;
+        if (dn) i -= items_gu;
+        const int per = dn ? tiles_dn : tiles_gu;
+        const int c = i / per;
+        if (c >= nchunks) return kMoeNoItem;
+        return (dn ? 1u << 31 : 0u) | static_cast<uint32_t>(c) << 22 | static_cast<uint32_t>(i - c * per);
+    };
+    if (taker) {
+        hd->claim[grp][0] = item_of(taken);
+        taken = atomicAdd(&a.cnt->claimed, 1);
+    }
+    group_sync<32 * GW>(grp);
+    int seq = 0;                                               // the current item is claim[seq % 4]
+    uint32_t cur = hd->claim[grp][0];
 
     uint32_t slot[kMoeRing];
 #pragma unroll
@@ -409,273 +450,315 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_codes,   // u8, 64
         const uint32_t i = static_cast<uint32_t>(warp * kMoeRing + s);
         slot[s] = i < nlow ? low0 + i * kMoeSlotBytes : kDsHighAddr + (i - nlow) * kMoeSlotBytes;
     }
-
-    // ---- requests: one step ahead of the computation, across items. A warp
-    // with gw >= nkc has no steps and only takes part in the joining of sums.
-    const bool any = gw < nkc;
     int issued = 0, landed = 0;
-    MoeWalk iw = item;
-    int ikc = gw, ic1 = 0, ic2 = 0;                            // box coordinates of iw's item
-    auto box_of = [&]() {
-        if (iw.chunk >= nchunks) return;
-        const int e = hd->chunk[iw.chunk].expert;
-        ic1 = DOWN ? e * a.H + iw.tile * kMoeRows : iw.tile * (kMoeRows / 2);
-        ic2 = 2 * e;
-    };
-    auto issue = [&]() {
-        if (!any || iw.chunk >= nchunks || abort_raised(abort_flag)) return;
+    // request one step's codes (kc-th 128 elements of the item's 64 rows)
+    auto issue = [&](uint32_t it, int kc) {
+        if (abort_raised(abort_flag)) return;
         if (lane == 0) {
             const int s = issued % kMoeRing;
             uint64_t *bar = &hd->bars[warp][s];
+            uint8_t *dst = dsm + (slot[s] - sbase);
+            const int e = hd->chunk[item_chunk(it)].expert, tile = item_tile(it);
             fence_proxy_async_smem();      // the slot was read through the generic proxy
             mbar_arrive_expect_tx(bar, kMoeSlotBytes);
-            if constexpr (DOWN) tma_load_2d(dsm + (slot[s] - sbase), &tm_codes, bar, ikc * kMoeStepBytes, ic1);
-            else tma_load_3d(dsm + (slot[s] - sbase), &tm_codes, bar, ikc * kMoeStepBytes, ic1, ic2);
+            if (item_down(it)) tma_load_2d(dst, &tm_down, bar, kc * kMoeStepBytes, e * a.H + tile * kMoeRows);
+            else tma_load_3d(dst, &tm_gate_up, bar, kc * kMoeStepBytes, tile * (kMoeRows / 2), 2 * e);
         }
         ++issued;
-        ikc += GW;
-        if (ikc >= nkc) {
-            ikc = gw;
-            iw.next(dchunk, dtile, tiles);
-            box_of();
-        }
     };
+    // the first step of this warp in an item whose rows have nkc steps; a warp
+    // beyond the last one takes it too and leaves its products out of the sums
+    auto first_step = [&](bool dn) { return min(gw, ((dn ? a.F : a.H) / kBlock + 1) / 2 - 1); };
 
     // Which row of a 16-row tile lane group g reads: with 64-byte rows under
     // the 64-byte swizzle, rows {0,1,4,5} (and {2,3,6,7}) of one block take
     // all 32 banks once.
     const int prow = (g & 1) | ((g & 2) << 1) | ((g & 4) >> 1);
-
-    // ---- operands of the next step: the raw scales of this lane's two rows
-    // (rows prow and prow + 8 of tile t) and the activations of its token g.
-    // Lanes beyond the chunk's tokens read its last token again: their columns
-    // of the products are never stored. After the group's last item the cursor
-    // stays where it is, so every load below is of something valid.
-    MoeWalk nw = item;
-    int nkc_at = gw;
-    const uint16_t *nx = nullptr;                              // x (or a) at token g, element 16 t
-    uint32_t nsb = 0;                                          // scale index of the first row; the second is 8 bpr on
-    auto operands_of = [&]() {
-        const MoeChunk c = hd->chunk[nw.chunk];
-        const int sl = c.slot0 + min(g, c.n - 1);
-        nx = (DOWN ? a.a + static_cast<int64_t>(sl) * K : a.x + static_cast<int64_t>(hd->token[sl]) * K) + 16 * t;
-        const int row = DOWN ? c.expert * a.H + nw.tile * kMoeRows + 16 * t
-                             : (c.expert * 2 + (t >> 1)) * a.F + nw.tile * (kMoeRows / 2) + 16 * (t & 1);
-        nsb = static_cast<uint32_t>(row + prow) * static_cast<uint32_t>(bpr);
-    };
-    auto next_operands = [&]() {
-        nkc_at += GW;
-        if (nkc_at >= nkc) {
-            MoeWalk w = nw;
-            w.next(dchunk, dtile, tiles);
-            if (w.chunk < nchunks) {
-                nw = w;
-                nkc_at = gw;
-                operands_of();
-            } else {
-                nkc_at -= GW;
-            }
-        }
-    };
-    uint32_t raw[2][PAIRS ? 1 : 2];                            // [row][block]: q8 codes, or the absmax bits
-    float grp_c[2][PAIRS ? 1 : 2];                             // their group constants
-    auto load_scales = [&]() {
-        const int b0 = 2 * nkc_at;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t at = nsb + static_cast<uint32_t>(8 * i * bpr + (b0 >> a.bshift));
-            if constexpr (PAIRS) {
-                raw[i][0] = __ldg(reinterpret_cast<const uint16_t *>(a.q8 + at));
-                grp_c[i][0] = __ldg(a.cg + (at >> 8));
-            } else {
-                // the second block of a step: its own scale, the same one (128-element
-                // blocks), or, behind the row's last block, not used
-                const uint32_t at1 = a.bshift || b0 + 1 >= kblocks ? at : at + 1;
-                if (a.dq) {
-                    raw[i][0] = __ldg(a.q8 + at);
-                    raw[i][1] = __ldg(a.q8 + at1);
-                    grp_c[i][0] = __ldg(a.cg + (at >> 8));
-                    grp_c[i][1] = __ldg(a.cg + (at1 >> 8));
-                } else {
-                    raw[i][0] = __float_as_uint(__ldg(a.absmax + at));
-                    raw[i][1] = __float_as_uint(__ldg(a.absmax + at1));
-                }
-            }
-        }
-    };
-    // (c / 127 by its reciprocal: one rounding away, and the sums are not compared bit for bit)
-    auto scale_of = [&](int i, int b) -> float {
-        if constexpr (PAIRS) {
-            const uint32_t q = b ? raw[i][0] >> 8 : raw[i][0] & 0xffu;
-            return static_cast<float>(q) * (grp_c[i][0] * (kMoeLevelDown / 127.0f));
-        } else {
-            return a.dq ? static_cast<float>(raw[i][b]) * (grp_c[i][b] * (kMoeLevelDown / 127.0f))
-                        : __uint_as_float(raw[i][b]) * kMoeLevelDown;
-        }
-    };
-    uint4 xv[2][2];                                            // [block][half]
-    auto load_x = [&](int b) {
-        const int blk = min(2 * nkc_at + b, kblocks - 1);
-        const uint4 *q = reinterpret_cast<const uint4 *>(nx + blk * kBlock);
-        xv[b][0] = q[0];
-        xv[b][1] = q[1];
-    };
-
     const uint32_t lanew = (static_cast<uint32_t>(lane) << 2) | (1u << 16);
     const uint32_t swz = static_cast<uint32_t>((prow >> 1) & 3);
     const uint32_t code_row = static_cast<uint32_t>(prow) * kMoeStepBytes + 8u * (t & 1);
     const uint32_t code_chunk[2] = {((0u + (t >> 1)) ^ swz) << 4, ((2u + (t >> 1)) ^ swz) << 4};
-    // this thread's place in the group's partial sums: lane's sums j and j + 8
-    // for j = gw, gw + GW, ... < 8 (j = 4 tile + element)
+    // sum j (= 4 tile + element) of warp w of this group, this thread's lane
     auto park = [&](int w, int j) {
         return reinterpret_cast<float *>(lut_g + ((grp * GW + w) * 16 + j) * 256 + 128 + 4 * lane);
     };
 
-    // down: the item before's place in the count of its stripe, looked at one
-    // item later, when the atomic has long returned
-    int seen = -1, seen_tile = 0;
-    auto combine = [&](int tile) {
-        // every slot's share of these 64 columns is there: each token's top_k
-        // of them are added in order
-        const int gt = gw * 32 + lane;
-        const int h = tile * kMoeRows + (gt & 63);
-        for (int m = gt >> 6; m < a.M; m += GW / 2) {
-            float v = 0.0f;
-            for (int j = 0; j < a.top_k; ++j)
-                v += __ldcg(a.y + static_cast<int64_t>(hd->slot_of[m * a.top_k + j]) * a.H + h);
-            const int64_t o = static_cast<int64_t>(m) * a.H + h;
-            if (a.residual) v += bf16_lo(a.residual[o]);
-            const __nv_bfloat16 b = __float2bfloat16_rn(v);
-            a.out[o] = *reinterpret_cast<const uint16_t *>(&b);
-        }
-    };
-
-    box_of();
-    issue();
-    if (any && item.chunk < nchunks) {
-        operands_of();
-        load_scales();
-        load_x(0);
-        load_x(1);
+    if (cur != kMoeNoItem) issue(cur, first_step(item_down(cur)));
+    if (taker) {
+        hd->claim[grp][1] = item_of(taken);
+        taken = atomicAdd(&a.cnt->claimed, 1);
     }
+    group_sync<32 * GW>(grp);
 
-    for (; item.chunk < nchunks; item.next(dchunk, dtile, tiles)) {
-        float acc[4][4];
+    // ---- the items of one kind, to the group's last of them
+    auto run = [&](auto down_c) {
+        constexpr bool DOWN = decltype(down_c)::value;
+        const MoeScales &sw = DOWN ? a.down : a.gate_up;
+        const int K = DOWN ? a.F : a.H;
+        const int kblocks = K / kBlock;
+        const int nkc = (kblocks + 1) / 2;                     // steps of an item
+        const int bpr = kblocks >> sw.bshift;                  // scale blocks of a weight row
+        const int kc0 = first_step(DOWN);
+        const bool real = gw < nkc;
+
+        // down: the group waits until the activations of a chunk are complete
+        // (one thread looks, with pauses: a thousand warps reading the same
+        // counters would hold up the atomics that they wait for). True once all
+        // chunks are known to be.
+        auto wait_chunk = [&](int chunk) -> bool {
+            if (taker) {
+                const long long t0 = clock64();
+                int st = 0;
+                while (true) {
+                    if (load_acquire_gpu(&a.cnt->gate_up_done) == items_gu) {
+                        st = 1;
+                        break;
+                    }
+                    if (load_acquire_gpu(&a.cnt->chunk_done[chunk]) == tiles_gu || abort_raised(abort_flag)) break;
+                    if (clock64() - t0 > kWaitLimitCycles) {
+                        record_status(NF4_ERR_TIMEOUT);
+                        *abort_flag = 1;
+                        break;
+                    }
+                    __nanosleep(100);
+                }
+                hd->ready[grp] = st;
+            }
+            group_sync<32 * GW>(grp);        // the thread's acquire holds for the group's loads below
+            return hd->ready[grp] != 0;
+        };
+
+        // operands of the next step: the raw scales of this lane's two rows
+        // (rows prow and prow + 8 of tile t) and the activations of its token g.
+        // Lanes beyond the chunk's tokens read its last token again: their
+        // columns of the products are never stored.
+        int nkc_at = kc0;
+        const uint16_t *nx = nullptr;                          // x (or a) at token g, element 16 t
+        uint32_t nsb = 0;                                      // scale index of the first row; the second is 8 bpr on
+        auto operands_of = [&](uint32_t it) {
+            const MoeChunk c = hd->chunk[item_chunk(it)];
+            const int sl = c.slot0 + min(g, c.n - 1);
+            nx = (DOWN ? a.a + static_cast<int64_t>(sl) * K : a.x + static_cast<int64_t>(hd->token[sl]) * K) + 16 * t;
+            const int row = DOWN ? c.expert * a.H + item_tile(it) * kMoeRows + 16 * t
+                                 : (c.expert * 2 + (t >> 1)) * a.F + item_tile(it) * (kMoeRows / 2) + 16 * (t & 1);
+            nsb = static_cast<uint32_t>(row + prow) * static_cast<uint32_t>(bpr);
+            nkc_at = kc0;
+        };
+        uint32_t raw[2][PAIRS ? 1 : 2];                        // [row][block]: q8 codes, or the absmax bits
+        float grp_c[2][PAIRS ? 1 : 2];                         // their group constants
+        auto load_scales = [&]() {
+            const int b0 = 2 * nkc_at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
-        for (int kc = gw; kc < nkc; kc += GW) {
-            float sc[2][2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) sc[i][b] = scale_of(i, b);
-            next_operands();
-            load_scales();
-            issue();
-            const int rs = landed % kMoeRing;
-            if (mbar_wait_warp(&hd->bars[warp][rs], static_cast<uint32_t>(landed / kMoeRing) & 1u, abort_flag)) ++landed;
-            const uint32_t cbase = slot[rs] + code_row + after_wait_zero();
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (b == 1 && 2 * kc + 1 >= kblocks) break;    // an odd row's last step is one block
-                uint2 cw[4][2];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int hi = 0; hi < 2; ++hi)
-                        cw[i][hi] = ds_lds64(cbase + (16 * i + 8 * hi) * kMoeStepBytes + code_chunk[b]);
-                float pp[4][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 &x4 = xv[b][q >> 1];
-                    const uint32_t b0 = (q & 1) ? x4.z : x4.x, b1 = (q & 1) ? x4.w : x4.y;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t wl = (q < 2) ? cw[i][0].x : cw[i][0].y;
-                        const uint32_t wh = (q < 2) ? cw[i][1].x : cw[i][1].y;
-                        uint32_t af[4];
-                        if (q & 1) {
-                            af[0] = ds_lut(ds_addr<2>(wl, lanew));
-                            af[1] = ds_lut(ds_addr<2>(wh, lanew));
-                            af[2] = ds_lut(ds_addr<3>(wl, lanew));
-                            af[3] = ds_lut(ds_addr<3>(wh, lanew));
-                        } else {
-                            af[0] = ds_lut(ds_addr<0>(wl, lanew));
-                            af[1] = ds_lut(ds_addr<0>(wh, lanew));
-                            af[2] = ds_lut(ds_addr<1>(wl, lanew));
-                            af[3] = ds_lut(ds_addr<1>(wh, lanew));
-                        }
-                        if (q == 0) ds_mma_zero(pp[i], af, b0, b1);
-                        else mma_bf16_16816(pp[i], af, b0, b1);
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t at = nsb + static_cast<uint32_t>(8 * i * bpr + (b0 >> sw.bshift));
+                if constexpr (PAIRS) {
+                    raw[i][0] = __ldg(reinterpret_cast<const uint16_t *>(sw.q8 + at));
+                    grp_c[i][0] = __ldg(sw.cg + (at >> 8));
+                } else {
+                    // the second block of a step: its own scale, the same one (128-element
+                    // blocks), or, behind the row's last block, not used
+                    const uint32_t at1 = sw.bshift || b0 + 1 >= kblocks ? at : at + 1;
+                    if (sw.dq) {
+                        raw[i][0] = __ldg(sw.q8 + at);
+                        raw[i][1] = __ldg(sw.q8 + at1);
+                        grp_c[i][0] = __ldg(sw.cg + (at >> 8));
+                        grp_c[i][1] = __ldg(sw.cg + (at1 >> 8));
+                    } else {
+                        raw[i][0] = __float_as_uint(__ldg(sw.absmax + at));
+                        raw[i][1] = __float_as_uint(__ldg(sw.absmax + at1));
                     }
                 }
-                load_x(b);              // the next step's, into the registers just read
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // rows prow and prow + 8 of tile i: lane (g, i) of this quad has their scales
-                    const float s0 = __shfl_sync(0xffffffffu, sc[0][b], (lane & ~3) | i);
-                    const float s1 = __shfl_sync(0xffffffffu, sc[1][b], (lane & ~3) | i);
-                    acc[i][0] = fmaf(s0, pp[i][0], acc[i][0]);
-                    acc[i][1] = fmaf(s0, pp[i][1], acc[i][1]);
-                    acc[i][2] = fmaf(s1, pp[i][2], acc[i][2]);
-                    acc[i][3] = fmaf(s1, pp[i][3], acc[i][3]);
-                }
             }
-            if (2 * kc + 1 >= kblocks) load_x(1);
-            __syncwarp();               // every lane has read the slot
-        }
+        };
+        // (c / 127 by its reciprocal: one rounding away, and the sums are not compared bit for bit)
+        auto scale_of = [&](int i, int b) -> float {
+            if constexpr (PAIRS) {
+                const uint32_t q = b ? raw[i][0] >> 8 : raw[i][0] & 0xffu;
+                return static_cast<float>(q) * (grp_c[i][0] * (kMoeLevelDown / 127.0f));
+            } else {
+                return sw.dq ? static_cast<float>(raw[i][b]) * (grp_c[i][b] * (kMoeLevelDown / 127.0f))
+                             : __uint_as_float(raw[i][b]) * kMoeLevelDown;
+            }
+        };
+        uint4 xv[2][2];                                        // [block][half]
+        auto load_x = [&](int b) {
+            const int blk = min(2 * nkc_at + b, kblocks - 1);
+            const uint4 *q = reinterpret_cast<const uint4 *>(nx + blk * kBlock);
+            xv[b][0] = q[0];
+            xv[b][1] = q[1];
+        };
 
-        // ---- the group's k splits meet in the odd halves of the table rows,
-        // and are added in warp order
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) *park(gw, i * 4 + e) = acc[i][e];
-        if (DOWN && gw == 0 && lane == 0) hd->last[grp] = seen == nchunks - 1;
-        group_sync<32 * GW>(grp);
-        if (DOWN && hd->last[grp]) combine(seen_tile);
-        const MoeChunk c = hd->chunk[item.chunk];
-#pragma unroll
-        for (int j = gw; j < 8; j += GW) {
-            float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-            for (int w = 0; w < GW; ++w) {
-                s0 += *park(w, j);
-                s1 += *park(w, j + 8);
+        // down: the item before's place in the count of its stripe, looked at
+        // one item later, when the atomic has long returned
+        int seen = -1, seen_tile = 0;
+        auto combine = [&](int tile) {
+            // every slot's share of these 64 columns is there: each token's
+            // top_k of them are added in order
+            const int gt = gw * 32 + lane;
+            const int h = tile * kMoeRows + (gt & 63);
+            for (int m = gt >> 6; m < a.M; m += GW / 2) {
+                float v = 0.0f;
+                for (int j = 0; j < a.top_k; ++j)
+                    v += __ldcg(a.y + static_cast<int64_t>(hd->slot_of[m * a.top_k + j]) * a.H + h);
+                const int64_t o = static_cast<int64_t>(m) * a.H + h;
+                if (a.residual) v += bf16_lo(a.residual[o]);
+                const __nv_bfloat16 b = __float2bfloat16_rn(v);
+                a.out[o] = *reinterpret_cast<const uint16_t *>(&b);
             }
-            const int e = j & 3;
-            const int rr = 16 * (j >> 2) + prow + 8 * (e >> 1), col = 2 * t + (e & 1);
-            if (col < c.n) {
-                if constexpr (!DOWN) {
-                    // s0 is gate row rr, s1 up row rr
-                    const __nv_bfloat16 v = __float2bfloat16_rn(act_value(s0, a.act) * s1);
-                    a.a[static_cast<int64_t>(c.slot0 + col) * a.F + item.tile * (kMoeRows / 2) + rr] =
-                        *reinterpret_cast<const uint16_t *>(&v);
-                } else {
-                    const float w = hd->weight[c.slot0 + col];
-                    float *y = a.y + static_cast<int64_t>(c.slot0 + col) * a.H + item.tile * kMoeRows + rr;
-                    __stcg(y, w * s0);
-                    __stcg(y + 32, w * s1);
+        };
+        // the thread that counts the group's finished items (not the one that
+        // takes them, whose atomics are on the way to the next)
+        const bool counter = gw == GW - 1 && lane == 0;
+
+        if (cur == kMoeNoItem || item_down(cur) != DOWN) return;
+        bool all_done = !DOWN, fetched = false;
+
+        while (cur != kMoeNoItem && item_down(cur) == DOWN) {
+            const uint32_t nxt = hd->claim[grp][(seq + 1) & 3];
+            if (!fetched) {
+                operands_of(cur);
+                load_scales();
+                if (DOWN && !all_done) all_done = wait_chunk(item_chunk(cur));
+                load_x(0);
+                load_x(1);
+            }
+            fetched = all_done && nxt != kMoeNoItem && item_down(nxt) == DOWN;
+            float acc[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
+            for (int kc = kc0; kc < nkc; kc += GW) {
+                float sc[2][2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) sc[i][b] = scale_of(i, b);
+                // the next step: of this item, or the first of the next one (its
+                // activations only when they are known to be complete)
+                if (kc + GW < nkc) {
+                    nkc_at += GW;
+                    issue(cur, kc + GW);
+                } else if (nxt != kMoeNoItem) {
+                    issue(nxt, first_step(item_down(nxt)));
+                    if (fetched) operands_of(nxt);
+                }
+                load_scales();
+                const int rs = landed % kMoeRing;
+                if (mbar_wait_warp(&hd->bars[warp][rs], static_cast<uint32_t>(landed / kMoeRing) & 1u, abort_flag)) ++landed;
+                const uint32_t cbase = slot[rs] + code_row + after_wait_zero();
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    if (b == 1 && 2 * kc + 1 >= kblocks) break;    // an odd row's last step is one block
+                    uint2 cw[4][2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int hi = 0; hi < 2; ++hi)
+                            cw[i][hi] = ds_lds64(cbase + (16 * i + 8 * hi) * kMoeStepBytes + code_chunk[b]);
+                    float pp[4][4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 &x4 = xv[b][q >> 1];
+                        const uint32_t b0 = (q & 1) ? x4.z : x4.x, b1 = (q & 1) ? x4.w : x4.y;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t wl = (q < 2) ? cw[i][0].x : cw[i][0].y;
+                            const uint32_t wh = (q < 2) ? cw[i][1].x : cw[i][1].y;
+                            uint32_t af[4];
+                            if (q & 1) {
+                                af[0] = ds_lut(ds_addr<2>(wl, lanew));
+                                af[1] = ds_lut(ds_addr<2>(wh, lanew));
+                                af[2] = ds_lut(ds_addr<3>(wl, lanew));
+                                af[3] = ds_lut(ds_addr<3>(wh, lanew));
+                            } else {
+                                af[0] = ds_lut(ds_addr<0>(wl, lanew));
+                                af[1] = ds_lut(ds_addr<0>(wh, lanew));
+                                af[2] = ds_lut(ds_addr<1>(wl, lanew));
+                                af[3] = ds_lut(ds_addr<1>(wh, lanew));
+                            }
+                            if (q == 0) ds_mma_zero(pp[i], af, b0, b1);
+                            else mma_bf16_16816(pp[i], af, b0, b1);
+                        }
+                    }
+                    load_x(b);              // the next step's, into the registers just read
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // rows prow and prow + 8 of tile i: lane (g, i) of this quad has their scales
+                        const float s0 = __shfl_sync(0xffffffffu, sc[0][b], (lane & ~3) | i);
+                        const float s1 = __shfl_sync(0xffffffffu, sc[1][b], (lane & ~3) | i);
+                        acc[i][0] = fmaf(s0, pp[i][0], acc[i][0]);
+                        acc[i][1] = fmaf(s0, pp[i][1], acc[i][1]);
+                        acc[i][2] = fmaf(s1, pp[i][2], acc[i][2]);
+                        acc[i][3] = fmaf(s1, pp[i][3], acc[i][3]);
+                    }
+                }
+                if (2 * kc + 1 >= kblocks) load_x(1);
+                __syncwarp();               // every lane has read the slot
+            }
+
+            // ---- the group's k splits meet in the odd halves of the table
+            // rows, and are added in warp order
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) *park(gw, i * 4 + e) = real ? acc[i][e] : 0.0f;
+            if (taker) {
+                hd->claim[grp][(seq + 2) & 3] = item_of(taken);
+                taken = atomicAdd(&a.cnt->claimed, 1);
+            }
+            if (DOWN && counter) hd->last[grp] = seen == nchunks - 1;
+            group_sync<32 * GW>(grp);
+            if (DOWN && hd->last[grp]) combine(seen_tile);
+            const MoeChunk c = hd->chunk[item_chunk(cur)];
+            const int tile = item_tile(cur);
+#pragma unroll
+            for (int j = gw; j < 8; j += GW) {
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int w = 0; w < GW; ++w) {
+                    s0 += *park(w, j);
+                    s1 += *park(w, j + 8);
+                }
+                const int e = j & 3;
+                const int rr = 16 * (j >> 2) + prow + 8 * (e >> 1), col = 2 * t + (e & 1);
+                if (col < c.n) {
+                    if constexpr (!DOWN) {
+                        // s0 is gate row rr, s1 up row rr
+                        const __nv_bfloat16 v = __float2bfloat16_rn(act_value(s0, a.act) * s1);
+                        a.a[static_cast<int64_t>(c.slot0 + col) * a.F + tile * (kMoeRows / 2) + rr] =
+                            *reinterpret_cast<const uint16_t *>(&v);
+                    } else {
+                        const float w = hd->weight[c.slot0 + col];
+                        float *y = a.y + static_cast<int64_t>(c.slot0 + col) * a.H + tile * kMoeRows + rr;
+                        __stcg(y, w * s0);
+                        __stcg(y + 32, w * s1);
+                    }
                 }
             }
-        }
-        group_sync<32 * GW>(grp);        // the partials are free again, the products written
-        if (DOWN) {
-            seen_tile = item.tile;
-            if (gw == 0 && lane == 0) {
-                __threadfence();         // the group's products before the count
-                seen = atomicAdd(a.done + item.tile, 1);
-                __threadfence();
+            group_sync<32 * GW>(grp);        // the partials are free again, the results written
+            seen_tile = tile;
+            if (counter) {
+                __threadfence();             // the group's results before the counts
+                if constexpr (DOWN) {
+                    seen = atomicAdd(a.cnt->stripe_done + tile, 1);
+                    __threadfence();         // the others' results after it
+                } else {
+                    atomicAdd(&a.cnt->chunk_done[item_chunk(cur)], 1);
+                    atomicAdd(&a.cnt->gate_up_done, 1);
+                }
             }
+            ++seq;
+            cur = nxt;
         }
-    }
-    if (DOWN) {
-        if (gw == 0 && lane == 0) hd->last[grp] = seen == nchunks - 1;
-        group_sync<32 * GW>(grp);
-        if (hd->last[grp]) combine(seen_tile);
-    }
+        if (DOWN) {
+            if (counter) hd->last[grp] = seen == nchunks - 1;
+            group_sync<32 * GW>(grp);
+            if (hd->last[grp]) combine(seen_tile);
+        }
+    };
+    run(std::integral_constant<bool, false>{});
+    run(std::integral_constant<bool, true>{});
     // leave no copy in flight into shared memory that is about to be released
     // (after a normal end every copy has landed)
     if (lane == 0)

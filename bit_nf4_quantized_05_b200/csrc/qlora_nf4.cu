@@ -52,13 +52,12 @@ nf4_status map_fail(int line) {
 // Optional per-kernel event timing (nf4_profiling / nf4_profile_read)
 // ---------------------------------------------------------------------------
 enum KernelKind {
-    KK_QUANTIZE, KK_DEQUANTIZE, KK_LORA_U, KK_LORA_V, KK_LORA_DBDA, KK_ZERO, KK_GEMM_FWD, KK_GEMM_DGRAD, KK_DECODE, KK_DECODE_U, KK_MERGE, KK_LORA_ADD, KK_EPI_BWD, KK_MOE_ROUTER, KK_MOE_GATE_UP, KK_MOE_DOWN,
+    KK_QUANTIZE, KK_DEQUANTIZE, KK_LORA_U, KK_LORA_V, KK_LORA_DBDA, KK_ZERO, KK_GEMM_FWD, KK_GEMM_DGRAD, KK_DECODE, KK_DECODE_U, KK_MERGE, KK_LORA_ADD, KK_EPI_BWD, KK_MOE_ROUTER, KK_MOE_EXPERTS,
     KK_COUNT
 };
 const char *const kKindNames[KK_COUNT] = {
     "nf4_quantize", "nf4_dequantize", "lora_u", "lora_v", "lora_dB_dA", "zero_fill", "qlora_gemm_fwd", "qlora_gemm_dgrad", "qlora_decode",
-    "decode_lora_u", "qlora_merge", "lora_dX_add", "epilogue_bwd", "moe_router", "moe_gate_up",
-    "moe_down"};
+    "decode_lora_u", "qlora_merge", "lora_dX_add", "epilogue_bwd", "moe_router", "moe_experts"};
 
 struct ProfRecord {
     int kind;
@@ -1398,15 +1397,16 @@ nf4_status qlora_linear_bwd_epilogue(const nf4_weight *w, const uint16_t *x, int
 namespace {
 
 struct MoeLayout {
-    size_t logits, route, done, a, y, total;
+    size_t logits, cnt, a, y, total;
 };
+
+int64_t moe_splits(int64_t H) { return (H + kMrSplit - 1) / kMrSplit; }
 
 MoeLayout moe_layout(int64_t M, int64_t E, int64_t H, int64_t F, int64_t top_k) {
     MoeLayout L{};
     size_t off = 0;
-    L.logits = off; off = align256(off + size_t(M) * E * 8);
-    L.route = off;  off = align256(off + sizeof(MoeRoute));
-    L.done = off;   off = align256(off + size_t(H / kMoeRows) * 4);
+    L.logits = off; off = align256(off + size_t(moe_splits(H)) * M * E * 8);
+    L.cnt = off;    off = align256(off + sizeof(MoeCounters) + size_t(H / kMoeRows) * 4);
     L.a = off;      off = align256(off + size_t(M) * top_k * F * 2);
     L.y = off;      off = align256(off + size_t(M) * top_k * H * 4);
     L.total = off;
@@ -1427,15 +1427,16 @@ bool make_map_3d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t mi
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Warps of a group: the choice with the smallest (rounds of items over the
-// groups) x (steps of a warp per item + 1), the 1 standing for what an item
-// costs beside its steps.
-int pick_moe_group(int64_t items, int64_t steps, int sms) {
+// Warps of a group: the choice with the smallest estimate of (items x (steps of
+// a warp per item + 1) over the groups, plus one item of each kind for the uneven
+// end), the 1 standing for what an item costs beside its steps.
+int pick_moe_group(double chunks, int64_t tiles_gu, int64_t steps_gu, int64_t tiles_dn, int64_t steps_dn, int sms) {
     int best = 4;
-    int64_t best_cost = -1;
+    double best_cost = -1;
     for (int gw : {4, 8, 16}) {
-        const int64_t groups = int64_t(sms) * (kMoeWarps / gw);
-        const int64_t cost = ((items + groups - 1) / groups) * ((steps + gw - 1) / gw + 1);
+        const double groups = double(sms) * (kMoeWarps / gw);
+        const double gu = double((steps_gu + gw - 1) / gw + 1), dn = double((steps_dn + gw - 1) / gw + 1);
+        const double cost = (chunks * tiles_gu / groups + 1) * gu + (chunks * tiles_dn / groups + 1) * dn;
         if (best_cost < 0 || cost < best_cost) {
             best = gw;
             best_cost = cost;
@@ -1444,33 +1445,31 @@ int pick_moe_group(int64_t items, int64_t steps, int sms) {
     return best;
 }
 
-template <bool DOWN>
-nf4_status launch_moe_experts(const nf4_weight *w, const MoeArgs &base, cudaStream_t s) {
-    MoeArgs a = base;
-    a.absmax = w->absmax;
-    a.q8 = w->absmax_q8;
-    a.cg = w->absmax_c;
-    a.dq = w->double_quant;
-    a.bshift = block_shift_of(w->block_size);
-    CUtensorMap tm;
-    const bool ok = DOWN ? make_map(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->codes, w->k / 2, w->n, kMoeStepBytes,
-                                    kMoeRows, CU_TENSOR_MAP_SWIZZLE_64B)
-                         : make_map_3d(&tm, w->codes, w->k / 2, a.F, 2 * a.E, kMoeStepBytes, kMoeRows / 2, 2,
-                                       CU_TENSOR_MAP_SWIZZLE_64B);
-    if (!ok) return map_fail(__LINE__);
-    // chunks: at least one per chosen expert; how many experts that is, only
-    // the device knows, so the rule takes the expected number of a router
-    // that spreads its tokens evenly
+MoeScales moe_scales(const nf4_weight *w) {
+    return {w->absmax, w->absmax_q8, w->absmax_c, w->double_quant, block_shift_of(w->block_size)};
+}
+
+nf4_status launch_moe_experts(const nf4_weight *gate_up, const nf4_weight *down, const MoeArgs &a, cudaStream_t s) {
+    CUtensorMap tm_gu, tm_dn;
+    if (!make_map_3d(&tm_gu, gate_up->codes, gate_up->k / 2, a.F, 2 * a.E, kMoeStepBytes, kMoeRows / 2, 2,
+                     CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_map(&tm_dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, down->codes, down->k / 2, down->n, kMoeStepBytes, kMoeRows,
+                  CU_TENSOR_MAP_SWIZZLE_64B))
+        return map_fail(__LINE__);
+    // at least one chunk per chosen expert; how many experts that is, only the
+    // device knows, so the rule takes the expected number of a router that
+    // spreads its tokens evenly
     const int sms = num_sms(current_device());
-    const double idle = std::pow(1.0 - double(a.top_k) / a.E, double(a.M));
-    const int64_t chunks = std::max<int64_t>(1, std::llround(a.E * (1.0 - idle)));
-    const int64_t tiles = DOWN ? a.H / kMoeRows : a.F / (kMoeRows / 2);
-    const int64_t steps = (w->k / kBlock + 1) / 2;
-    const int gw = pick_moe_group(chunks * tiles, steps, sms);
-    const bool pairs = w->double_quant && w->block_size == 64 && w->k / kBlock % 2 == 0;
-    auto kern = nf4_moe_experts_kernel<DOWN, 4, true>;
+    const double chunks = std::max(1.0, a.E * (1.0 - std::pow(1.0 - double(a.top_k) / a.E, double(a.M))));
+    const int gw = pick_moe_group(chunks, a.F / (kMoeRows / 2), (a.H / kBlock + 1) / 2, a.H / kMoeRows,
+                                  (a.F / kBlock + 1) / 2, sms);
+    auto in_pairs = [](const nf4_weight *w) {
+        return w->double_quant && w->block_size == 64 && w->k / kBlock % 2 == 0;
+    };
+    const bool pairs = in_pairs(gate_up) && in_pairs(down);
+    auto kern = nf4_moe_experts_kernel<4, true>;
 #define NF4_MOE_CASE(GW_, PAIRS_) \
-    if (gw == GW_ && pairs == PAIRS_) kern = nf4_moe_experts_kernel<DOWN, GW_, PAIRS_>;
+    if (gw == GW_ && pairs == PAIRS_) kern = nf4_moe_experts_kernel<GW_, PAIRS_>;
     NF4_MOE_CASE(8, true)
     NF4_MOE_CASE(16, true)
     NF4_MOE_CASE(4, false)
@@ -1478,9 +1477,9 @@ nf4_status launch_moe_experts(const nf4_weight *w, const MoeArgs &base, cudaStre
     NF4_MOE_CASE(16, false)
 #undef NF4_MOE_CASE
     NF4_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDsDynBytes));
-    LaunchTimer t(DOWN ? KK_MOE_DOWN : KK_MOE_GATE_UP, s);
+    LaunchTimer t(KK_MOE_EXPERTS, s);
     const cudaError_t e =
-        launch_ex(kern, dim3(static_cast<unsigned>(sms)), dim3(kMoeThreads), kDsDynBytes, s, 0u, tm, a);
+        launch_ex(kern, dim3(static_cast<unsigned>(sms)), dim3(kMoeThreads), kDsDynBytes, s, 0u, tm_gu, tm_dn, a);
     t.stop();
     if (e != cudaSuccess) return cuda_fail(e, __LINE__);
     NF4_TRY_CUDA(cudaGetLastError());
@@ -1538,23 +1537,24 @@ nf4_status nf4_moe_fwd(const nf4_weight *gate_up, const nf4_weight *down, const 
     a.out = out;
     a.ids = topk_ids;
     a.weights = topk_weights;
+    a.gate_up = moe_scales(gate_up);
+    a.down = moe_scales(down);
+    a.splits = static_cast<int>(moe_splits(H));
     a.logits = reinterpret_cast<double *>(ws + L.logits);
-    a.route = reinterpret_cast<MoeRoute *>(ws + L.route);
+    a.cnt = reinterpret_cast<MoeCounters *>(ws + L.cnt);
     a.a = reinterpret_cast<uint16_t *>(ws + L.a);
     a.y = reinterpret_cast<float *>(ws + L.y);
-    a.done = reinterpret_cast<int *>(ws + L.done);
     {
         LaunchTimer t(KK_MOE_ROUTER, s);
         const cudaError_t e = launch_ex(nf4_moe_router_kernel,
                                         dim3(static_cast<unsigned>((E + kMrExperts - 1) / kMrExperts),
-                                             static_cast<unsigned>((M + kMrTokens - 1) / kMrTokens)),
+                                             static_cast<unsigned>((M + kMrTokens - 1) / kMrTokens),
+                                             static_cast<unsigned>(a.splits)),
                                         dim3(kMrThreads), 0, s, 0u, a);
         t.stop();
         if (e != cudaSuccess) return cuda_fail(e, __LINE__);
     }
-    st = launch_moe_experts<false>(gate_up, a, s);
-    if (st != NF4_OK) return st;
-    return launch_moe_experts<true>(down, a, s);
+    return launch_moe_experts(gate_up, down, a, s);
 }
 
 }  // extern "C"
