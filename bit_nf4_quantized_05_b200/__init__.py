@@ -228,17 +228,19 @@ class QuantizedWeight:
         if self.block_size not in (64, 128):
             raise ValueError("block_size must be 64 or 128")
         nb = self.n * self.k // self.block_size
-        need = [("codes", self.codes, torch.uint8, self.n * self.k // 2),
-                ("absmax", self.absmax, torch.float32, nb)]
+        dev = self.codes.get_device()
+        self._check_array("codes", self.codes, torch.uint8, self.n * self.k // 2, dev)
+        self._check_array("absmax", self.absmax, torch.float32, nb, dev)
         if self.double_quant:
-            need += [("absmax_q8", self.absmax_q8, torch.uint8, nb),
-                     ("absmax_c", self.absmax_c, torch.float32, (nb + 255) // 256)]
-        for name, t, dtype, count in need:
-            if t is None:
-                raise ValueError(f"{name} is required")
-            if t.dtype != dtype or not t.is_contiguous() or t.numel() < count or t.device != self.device:
-                raise ValueError(f"{name}: expected a contiguous {dtype} tensor of at least {count} "
-                                 f"entries on {self.device}")
+            self._check_array("absmax_q8", self.absmax_q8, torch.uint8, nb, dev)
+            self._check_array("absmax_c", self.absmax_c, torch.float32, (nb + 255) // 256, dev)
+
+    def _check_array(self, name: str, t: Optional[torch.Tensor], dtype, count: int, dev: int) -> None:
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if t.dtype is not dtype or t.numel() < count or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of at least {count} "
+                             f"entries on {self.device}")
 
     @staticmethod
     def empty(n: int, k: int, double_quant: bool, device, block_size: int = BLOCK_SIZE) -> "QuantizedWeight":
@@ -551,19 +553,58 @@ def _act(name: str) -> int:
     return ACTIVATIONS[name]
 
 
-def _on(device: torch.device):
-    """The device made current for a call (the library launches on the current one)."""
-    return torch.cuda.device(device)
+# A call's host time is part of a decoding step's, so the entry points below check
+# each tensor in one expression and spell out what is wrong only when something is.
+def _fits(t: torch.Tensor, shape: tuple, dtype, dev: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
-def _epilogue(qw: QuantizedWeight, M: int, act: str, bias, mul, residual) -> EpilogueStruct:
-    if bias is not None:
-        _check_t("bias", bias, (qw.n,), torch.bfloat16, qw.device)
-    for name, t in (("mul", mul), ("residual", residual)):
-        if t is not None:
-            _check_t(name, t, (M, qw.n), torch.bfloat16, qw.device)
-    p = lambda t: None if t is None else t.data_ptr()
-    return EpilogueStruct(_act(act), p(bias), p(mul), p(residual))
+def _check_fast(name: str, t: Optional[torch.Tensor], shape: tuple, dtype, qw: "QuantizedWeight", dev: int) -> None:
+    if t is not None and not _fits(t, shape, dtype, dev):
+        _check_t(name, t, shape, dtype, qw.device)
+
+
+class _OnDevice:
+    """Makes a device current for a call (the library launches on the current one)."""
+    __slots__ = ("dev", "prev")
+
+    def __init__(self, dev: int):
+        self.dev = dev
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.prev)
+
+
+# the current stream's handle without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _layer_fast(qw: "QuantizedWeight", x: torch.Tensor, A: torch.Tensor, B: torch.Tensor) -> Tuple[int, int, int]:
+    """(M, r, device index) of the checked x [M, k], A [r, k] and B [n, r]."""
+    dev, bf16 = qw.codes.get_device(), torch.bfloat16
+    if x.dim() == 2 and A.dim() == 2:
+        M, r = x.shape[0], A.shape[0]
+        if _fits(x, (M, qw.k), bf16, dev) and _fits(A, (r, qw.k), bf16, dev) and _fits(B, (qw.n, r), bf16, dev):
+            return M, r, dev
+    return _layer_args(qw, x, A, B) + (dev,)
+
+
+def _epilogue(qw: QuantizedWeight, M: int, act: str, bias, mul, residual, dev: int) -> EpilogueStruct:
+    _check_fast("bias", bias, (qw.n,), torch.bfloat16, qw, dev)
+    _check_fast("mul", mul, (M, qw.n), torch.bfloat16, qw, dev)
+    _check_fast("residual", residual, (M, qw.n), torch.bfloat16, qw, dev)
+    return EpilogueStruct(_act(act), _addr(bias), _addr(mul), _addr(residual))
 
 
 def qlora_linear_fwd_epilogue(qw: QuantizedWeight, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
@@ -580,23 +621,22 @@ def qlora_linear_fwd_epilogue(qw: QuantizedWeight, x: torch.Tensor, A: torch.Ten
     qlora_linear_bwd_epilogue takes. For act "relu" with save_z the sum is formed
     more exactly, at twice the products (see the C header). workspace: at least
     fwd_epilogue_workspace_bytes."""
-    M, r = _layer_args(qw, x, A, B)
-    ep = _epilogue(qw, M, act, bias, mul, residual)
-    if h is not None:
-        _check_t("h", h, (M, qw.n), torch.bfloat16, qw.device)
-    _check_ws(workspace, qw.device)
-    _need_cuda(x, A, B)
-    with _on(qw.device):
+    M, r, dev = _layer_fast(qw, x, A, B)
+    ep = _epilogue(qw, M, act, bias, mul, residual, dev)
+    _check_fast("h", h, (M, qw.n), torch.bfloat16, qw, dev)
+    _check_ws(workspace, qw.device if workspace is not None else None)
+    _need_cuda(x)
+    with _OnDevice(dev):
         if h is None:
-            h = torch.empty(M, qw.n, dtype=torch.bfloat16, device=x.device)
-        u = torch.empty(M, r, dtype=torch.float32, device=x.device) if save_u else None
-        z = torch.empty(M, qw.n, dtype=torch.bfloat16, device=x.device) if save_z else None
-        ws = workspace if workspace is not None else _workspace(
-            fwd_epilogue_workspace_bytes(M, qw.n, qw.k, r), x.device)
-        s = qw.struct()
-        _check(lib.qlora_linear_fwd_epilogue(ctypes.byref(s), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha),
-                                             ctypes.byref(ep), _ptr(h), _ptr(z), _ptr(u), _ptr(ws), ws.numel(),
-                                             _stream(x.device)), "qlora_linear_fwd_epilogue")
+            h = x.new_empty((M, qw.n))
+        u = x.new_empty((M, r), dtype=torch.float32) if save_u else None
+        z = x.new_empty((M, qw.n)) if save_z else None
+        if workspace is None:
+            workspace = _workspace(fwd_epilogue_workspace_bytes(M, qw.n, qw.k, r), x.device)
+        _check(lib.qlora_linear_fwd_epilogue(ctypes.byref(qw.struct()), x.data_ptr(), M, A.data_ptr(), B.data_ptr(),
+                                             r, alpha, ctypes.byref(ep), h.data_ptr(), _addr(z), _addr(u),
+                                             workspace.data_ptr(), workspace.numel(), _raw_stream(dev)),
+               "qlora_linear_fwd_epilogue")
     return h, u, z
 
 
@@ -619,33 +659,30 @@ def qlora_linear_bwd_epilogue(qw: QuantizedWeight, x: torch.Tensor, A: torch.Ten
     z and u are what the forward returned (z may be None for act "none" without
     mul; u is recomputed when None). The residual's gradient is dH itself.
     grad_dtype (bf16 or fp32) is the dtype of dA, dB and dbias."""
-    M, r = _layer_args(qw, x, A, B)
-    ep = _epilogue(qw, M, act, None, mul, None)
-    _check_t("dH", dH, (M, qw.n), torch.bfloat16, qw.device)
-    if z is not None:
-        _check_t("z", z, (M, qw.n), torch.bfloat16, qw.device)
-    elif act != "none" or mul is not None:
+    M, r, dev = _layer_fast(qw, x, A, B)
+    ep = _epilogue(qw, M, act, None, mul, None, dev)
+    _check_fast("dH", dH, (M, qw.n), torch.bfloat16, qw, dev)
+    _check_fast("z", z, (M, qw.n), torch.bfloat16, qw, dev)
+    if z is None and (act != "none" or mul is not None):
         raise ValueError("z (the forward's pre-activation) is required")
-    if u is not None:
-        _check_t("u", u, (M, r), torch.float32, qw.device)
+    _check_fast("u", u, (M, r), torch.float32, qw, dev)
     if grad_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("adapter gradients are bf16 or fp32")
-    _check_ws(workspace, qw.device)
-    _need_cuda(x, A, B, dH)
-    with _on(qw.device):
-        dX = torch.empty(M, qw.k, dtype=torch.bfloat16, device=x.device) if need_dX else None
-        dA = torch.empty(r, qw.k, dtype=grad_dtype, device=x.device)
-        dB = torch.empty(qw.n, r, dtype=grad_dtype, device=x.device)
-        dbias = torch.empty(qw.n, dtype=grad_dtype, device=x.device) if need_dbias else None
-        dmul = torch.empty(M, qw.n, dtype=torch.bfloat16, device=x.device) if mul is not None else None
-        ws = workspace if workspace is not None else _workspace(
-            bwd_epilogue_workspace_bytes(M, qw.n, qw.k, r), x.device)
-        s = qw.struct()
-        _check(lib.qlora_linear_bwd_epilogue(ctypes.byref(s), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha),
-                                             ctypes.byref(ep), _ptr(dH), _ptr(z), _ptr(u), _ptr(dX), _ptr(dA),
-                                             _ptr(dB), _ptr(dbias), _ptr(dmul), int(grad_dtype == torch.float32),
-                                             _ptr(ws), ws.numel(), _stream(x.device)),
-               "qlora_linear_bwd_epilogue")
+    _check_ws(workspace, qw.device if workspace is not None else None)
+    _need_cuda(x)
+    with _OnDevice(dev):
+        dX = x.new_empty((M, qw.k)) if need_dX else None
+        dA = x.new_empty((r, qw.k), dtype=grad_dtype)
+        dB = x.new_empty((qw.n, r), dtype=grad_dtype)
+        dbias = x.new_empty((qw.n,), dtype=grad_dtype) if need_dbias else None
+        dmul = x.new_empty((M, qw.n)) if mul is not None else None
+        if workspace is None:
+            workspace = _workspace(bwd_epilogue_workspace_bytes(M, qw.n, qw.k, r), x.device)
+        _check(lib.qlora_linear_bwd_epilogue(ctypes.byref(qw.struct()), x.data_ptr(), M, A.data_ptr(), B.data_ptr(),
+                                             r, alpha, ctypes.byref(ep), dH.data_ptr(), _addr(z), _addr(u),
+                                             _addr(dX), dA.data_ptr(), dB.data_ptr(), _addr(dbias), _addr(dmul),
+                                             grad_dtype is torch.float32, workspace.data_ptr(), workspace.numel(),
+                                             _raw_stream(dev)), "qlora_linear_bwd_epilogue")
     return dX, dA, dB, dbias, dmul
 
 
@@ -666,32 +703,31 @@ def nf4_moe_fwd(gate_up: QuantizedWeight, down: QuantizedWeight, x: torch.Tensor
     rule. out may be the residual itself."""
     if x.dim() != 2 or router.dim() != 2:
         raise ValueError("x and router must be 2-D")
-    M, H, E = x.shape[0], gate_up.k, router.shape[0]
-    _check_t("x", x, (M, H), torch.bfloat16, gate_up.device)
-    _check_t("router", router, (E, H), torch.bfloat16, gate_up.device)
+    M, H, E, dev = x.shape[0], gate_up.k, router.shape[0], gate_up.codes.get_device()
+    _check_fast("x", x, (M, H), torch.bfloat16, gate_up, dev)
+    _check_fast("router", router, (E, H), torch.bfloat16, gate_up, dev)
     if not 1 <= top_k <= E:
         raise ValueError(f"top_k must be between 1 and the {E} experts, got {top_k}")
-    if down.device != gate_up.device:
+    if down.codes.get_device() != dev:
         raise ValueError(f"down is on {down.device}, gate_up on {gate_up.device}")
     if gate_up.n != E * 2 * down.k or down.n != E * H:
         raise ValueError(f"gate_up [{gate_up.n}, {gate_up.k}] and down [{down.n}, {down.k}] are not {E} stacked "
                          "experts: expected [E * 2 * ffn, hidden] and [E * hidden, ffn]")
-    for name, t in (("residual", residual), ("out", out)):
-        if t is not None:
-            _check_t(name, t, (M, H), torch.bfloat16, gate_up.device)
-    _check_ws(workspace, gate_up.device)
-    _need_cuda(x, router)
-    with _on(gate_up.device):
+    _check_fast("residual", residual, (M, H), torch.bfloat16, gate_up, dev)
+    _check_fast("out", out, (M, H), torch.bfloat16, gate_up, dev)
+    _check_ws(workspace, gate_up.device if workspace is not None else None)
+    _need_cuda(x)
+    with _OnDevice(dev):
         if out is None:
-            out = torch.empty(M, H, dtype=torch.bfloat16, device=x.device)
-        ids = torch.empty(M, top_k, dtype=torch.int32, device=x.device)
-        weights = torch.empty(M, top_k, dtype=torch.float32, device=x.device)
-        ws = workspace if workspace is not None else _workspace(
-            moe_workspace_bytes(M, E, H, down.k, top_k), x.device)
-        sg, sd = gate_up.struct(), down.struct()
-        _check(lib.nf4_moe_fwd(ctypes.byref(sg), ctypes.byref(sd), _ptr(x), M, _ptr(router), E, int(top_k),
-                               int(bool(renormalise)), _act(act), _ptr(residual), _ptr(out), _ptr(ids),
-                               _ptr(weights), _ptr(ws), ws.numel(), _stream(x.device)), "nf4_moe_fwd")
+            out = x.new_empty((M, H))
+        ids = x.new_empty((M, top_k), dtype=torch.int32)
+        weights = x.new_empty((M, top_k), dtype=torch.float32)
+        if workspace is None:
+            workspace = _workspace(moe_workspace_bytes(M, E, H, down.k, top_k), x.device)
+        _check(lib.nf4_moe_fwd(ctypes.byref(gate_up.struct()), ctypes.byref(down.struct()), x.data_ptr(), M,
+                               router.data_ptr(), E, top_k, bool(renormalise), _act(act), _addr(residual),
+                               out.data_ptr(), ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(),
+                               workspace.numel(), _raw_stream(dev)), "nf4_moe_fwd")
     return out, ids, weights
 
 
