@@ -33,6 +33,26 @@ __device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0
 constexpr float kGeluTanhScale = 1.59576912160573f;    // 2 sqrt(2 / pi)
 constexpr float kGeluTanhCubic = 0.044715f;
 
+// Normal distribution function. With x = |z| / sqrt 2 and t = 1 / (1 + x / 2),
+//   erfc(x) = t 2^(-x^2 log2(e) + Q(t)),
+// where Q is a degree-7 Chebyshev fit of log2(erfc(x) e^(x^2) / t) over
+// 0.08 <= t <= 1: 1e-6 relative, also where erfc itself is tiny (beyond |z| =
+// 32 both are 0 in fp32). One reciprocal and one exponential; erfcf took 2.5
+// times the output step's time.
+__device__ __forceinline__ float normal_cdf(float z) {
+    const float t = __fdividef(1.0f, fmaf(0.35355339059327376f, fabsf(z), 1.0f));
+    float q = -0.27331653237342834f;
+    q = fmaf(q, t, 1.0946335792541504f);
+    q = fmaf(q, t, -1.4626392126083374f);
+    q = fmaf(q, t, 0.5222470164299011f);
+    q = fmaf(q, t, -0.06672894954681396f);
+    q = fmaf(q, t, 0.5712890028953552f);
+    q = fmaf(q, t, 1.4401801824569702f);
+    q = fmaf(q, t, -1.8256661891937256f - 1.0f);        // the - 1 halves erfc
+    const float tail = t * exp2f(fmaf(-0.72134752044448170f * z, z, q));
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
 __device__ __forceinline__ float act_value(float z, int act) {
     switch (act) {
         case NF4_ACT_RELU: return z < 0.0f ? 0.0f : z;
@@ -40,8 +60,23 @@ __device__ __forceinline__ float act_value(float z, int act) {
         // (1 + tanh(v / 2)) / 2 = logistic(v)
         case NF4_ACT_GELU_TANH:
             return z * logistic(kGeluTanhScale * fmaf(kGeluTanhCubic * z * z, z, z));
-        case NF4_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+        case NF4_ACT_GELU: return z * normal_cdf(z);
         default: return z;
+    }
+}
+
+__device__ __forceinline__ void act8(float (&f)[8], int act) {
+    switch (act) {
+#define NF4_ACT8(A_)                                      \
+    case A_:                                              \
+        _Pragma("unroll") for (int i = 0; i < 8; ++i) f[i] = act_value(f[i], A_); \
+        break;
+        NF4_ACT8(NF4_ACT_RELU)
+        NF4_ACT8(NF4_ACT_SILU)
+        NF4_ACT8(NF4_ACT_GELU_TANH)
+        NF4_ACT8(NF4_ACT_GELU)
+#undef NF4_ACT8
+        default: break;
     }
 }
 
@@ -67,7 +102,7 @@ __device__ __forceinline__ void act_pair(float z, int act, float &a, float &da) 
             return;
         }
         case NF4_ACT_GELU: {
-            const float cdf = 0.5f * erfcf(-0.70710678118654752f * z);
+            const float cdf = normal_cdf(z);
             a = z * cdf;
             da = fmaf(z, 0.39894228040143268f * __expf(-0.5f * z * z), cdf);
             return;
@@ -75,6 +110,22 @@ __device__ __forceinline__ void act_pair(float z, int act, float &a, float &da) 
         default:
             a = z;
             da = 1.0f;
+    }
+}
+
+__device__ __forceinline__ void act_pair8(const float (&z)[8], int act, float (&a)[8], float (&da)[8]) {
+    switch (act) {
+#define NF4_ACT_PAIR8(A_)                                 \
+    case A_:                                              \
+        _Pragma("unroll") for (int i = 0; i < 8; ++i) act_pair(z[i], A_, a[i], da[i]); \
+        break;
+        NF4_ACT_PAIR8(NF4_ACT_RELU)
+        NF4_ACT_PAIR8(NF4_ACT_SILU)
+        NF4_ACT_PAIR8(NF4_ACT_GELU_TANH)
+        NF4_ACT_PAIR8(NF4_ACT_GELU)
+        default:
+            NF4_ACT_PAIR8(NF4_ACT_NONE)
+#undef NF4_ACT_PAIR8
     }
 }
 
@@ -99,35 +150,38 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// The output step on eight consecutive columns [col, col + 8) of one row: f
-// comes as the fp32 sum and leaves as h. mul and residual may be the output
+// The output step on eight consecutive columns [col, col + 8) of one row: its
+// operands, then f from the fp32 sum to h. mul and residual may be the output
 // itself: the thread that reads an element is the one that then writes it, so
 // these are plain loads.
-__device__ __forceinline__ void epilogue8(const EpiArgs &e, int row, int N, int col, float (&f)[8]) {
-    const int64_t o = static_cast<int64_t>(row) * N + col;
-    uint4 mv, rv;
-    if (e.mul) mv = *reinterpret_cast<const uint4 *>(e.mul + o);
-    if (e.residual) rv = *reinterpret_cast<const uint4 *>(e.residual + o);
+struct EpiOperands {
+    uint4 bias, mul, residual;
+    __device__ __forceinline__ void load(const EpiArgs &e, int row, int N, int col) {
+        const int64_t o = static_cast<int64_t>(row) * N + col;
+        if (e.mul) mul = *reinterpret_cast<const uint4 *>(e.mul + o);
+        if (e.residual) residual = *reinterpret_cast<const uint4 *>(e.residual + o);
+        if (e.bias) bias = __ldg(reinterpret_cast<const uint4 *>(e.bias + col));
+    }
+};
+
+__device__ __forceinline__ void epilogue8(const EpiArgs &e, const EpiOperands &op, int64_t o, float (&f)[8]) {
+    float v[8];
     if (e.bias) {
-        float b[8];
-        bf16_unpack8(__ldg(reinterpret_cast<const uint4 *>(e.bias + col)), b);
+        bf16_unpack8(op.bias, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += b[i];
+        for (int i = 0; i < 8; ++i) f[i] += v[i];
     }
     if (e.z) *reinterpret_cast<uint4 *>(e.z + o) = bf16_pack8(f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = act_value(f[i], e.act);
+    act8(f, e.act);
     if (e.mul) {
-        float m[8];
-        bf16_unpack8(mv, m);
+        bf16_unpack8(op.mul, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= m[i];
+        for (int i = 0; i < 8; ++i) f[i] *= v[i];
     }
     if (e.residual) {
-        float r[8];
-        bf16_unpack8(rv, r);
+        bf16_unpack8(op.residual, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += r[i];
+        for (int i = 0; i < 8; ++i) f[i] += v[i];
     }
 }
 
@@ -157,7 +211,7 @@ struct EpiBwdArgs {
     int dbias_f32;
 };
 
-__global__ void __launch_bounds__(kEbThreads)
+__global__ void __launch_bounds__(kEbThreads, 2)
 qlora_epilogue_bwd_kernel(const EpiBwdArgs a) {
     __shared__ float part[kEbRows][kEbCols + 4];
     griddep_wait();
@@ -167,31 +221,45 @@ qlora_epilogue_bwd_kernel(const EpiBwdArgs a) {
     const int64_t step = static_cast<int64_t>(gridDim.x) * kEbRows;
     float sum[8] = {};
     if (col < a.N) {
-#pragma unroll 2
-        for (int64_t m = static_cast<int64_t>(blockIdx.x) * kEbRows + r; m < a.M; m += step) {
-            const int64_t o = m * a.N + col;
-            float g[8];
-            bf16_unpack8(__ldg(reinterpret_cast<const uint4 *>(a.dH + o)), g);
-            if (a.dz || a.dmul) {
-                uint4 mv = make_uint4(0, 0, 0, 0), zv = mv;
-                if (a.z) zv = __ldg(reinterpret_cast<const uint4 *>(a.z + o));
-                if (a.mul) mv = __ldg(reinterpret_cast<const uint4 *>(a.mul + o));
-                float z[8], f[8], dm[8];
-                bf16_unpack8(zv, z);
-                bf16_unpack8(mv, f);
+        // two rows in flight per thread
+        for (int64_t m = static_cast<int64_t>(blockIdx.x) * kEbRows + r; m < a.M; m += 2 * step) {
+            uint4 gv[2], zv[2], mv[2];
+            bool ok[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float v, d;
-                    act_pair(z[e], a.act, v, d);
-                    dm[e] = g[e] * v;
-                    if (a.mul) g[e] *= f[e];
-                    g[e] *= d;
-                }
-                if (a.dmul) *reinterpret_cast<uint4 *>(a.dmul + o) = bf16_pack8(dm);
-                if (a.dz) *reinterpret_cast<uint4 *>(a.dz + o) = bf16_pack8(g);
+            for (int i = 0; i < 2; ++i) {
+                const int64_t mi = m + i * step;
+                ok[i] = mi < a.M;
+                const int64_t o = (ok[i] ? mi : m) * a.N + col;
+                gv[i] = *reinterpret_cast<const uint4 *>(a.dH + o);
+                if (a.z) zv[i] = *reinterpret_cast<const uint4 *>(a.z + o);
+                if (a.mul) mv[i] = *reinterpret_cast<const uint4 *>(a.mul + o);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += g[e];
+            for (int i = 0; i < 2; ++i) {
+                if (!ok[i]) break;
+                const int64_t o = (m + i * step) * a.N + col;
+                float g[8];
+                bf16_unpack8(gv[i], g);
+                if (a.dz || a.dmul) {
+                    float z[8] = {}, f[8], dm[8];
+                    if (a.z) bf16_unpack8(zv[i], z);
+                    act_pair8(z, a.act, dm, f);               // act, act'
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        dm[e] *= g[e];
+                        g[e] *= f[e];
+                    }
+                    if (a.mul) {
+                        bf16_unpack8(mv[i], f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) g[e] *= f[e];
+                    }
+                    if (a.dmul) *reinterpret_cast<uint4 *>(a.dmul + o) = bf16_pack8(dm);
+                    if (a.dz) *reinterpret_cast<uint4 *>(a.dz + o) = bf16_pack8(g);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += g[e];
+            }
         }
     }
     if (!a.dbias) return;

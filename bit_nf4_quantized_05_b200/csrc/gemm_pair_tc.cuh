@@ -78,7 +78,6 @@ struct GemmArgs {
     float *D32;         // when non-null: the fp32 result goes here instead of D
     int bshift;         // log2(block size / 64): block of step j is j >> bshift
     EpiArgs epi;        // the output step of the EPI instantiations
-    int twice;          // EPI: every reduction step also with what rounding the operand left
 };
 
 template <int BN, bool DGRAD, int G>
@@ -250,14 +249,14 @@ __device__ __forceinline__ void set_flag_gpu(int *flag) {
 // L2 while the tile's products still run: an output thread reads 32 bytes of
 // its row per 16 columns, and sixteen such reads from HBM in a row would take
 // longer than the tile.
-// EPI with args.twice: each reduction step is followed by a second one on the
+// TWICE: each reduction step is followed by a second one on the
 // same activations with the rest of the weight, bf16(w - bf16(w)), and each
 // adapter step by one with the rest of the rank-r activations, so that the sum
 // has the weight to 2^-17 rather than 2^-9. A gradient that jumps at z = 0
 // needs that: an error d in z turns the sign of a share d / (3 std(z)) of the
 // elements, and each of those is wrong by its whole size (at 5120 x 5120, one
 // pass left dX 3.2% off in the 2-norm, two leave it at its output's rounding).
-template <int BN, bool DGRAD, int G, bool OUT32, bool EPI = false>
+template <int BN, bool DGRAD, int G, bool OUT32, bool EPI = false, bool TWICE = false>
 __global__ void __launch_bounds__(PairCfg<BN, DGRAD, G>::kThreads, 1)
 qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red] bf16, box {64,128}
                        const __grid_constant__ CUtensorMap tm_codes,  // [Nw, K/2] u8, box {32, rows}
@@ -331,7 +330,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
     const int m_pairs = (args.M + 2 * kBM - 1) / (2 * kBM);
     const int total_tiles = m_pairs * args.n_tiles;
     // reduction step `it` is step it >> ps of the operands; its low bit selects the rest
-    const int ps = EPI ? args.twice : 0;
+    constexpr int ps = TWICE ? 1 : 0;
     const int main_steps = args.main_steps << ps;
     const int nsteps = main_steps + (args.lora_steps << ps);
     PairSched sched;
@@ -507,6 +506,38 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
                     pp = args.partial + static_cast<int64_t>(src) * kChunks * (128 * 32) + rloc * 32;
                 }
                 const int row = m0 + rloc;
+                if constexpr (EPI) {
+                    // 8 columns at a time: the operands of the output step take the
+                    // registers that the plain form spends on 16
+#pragma unroll 1
+                    for (int c8 = 0; c8 < BN / 8; ++c8) {
+                        const int col = n0 + c8 * 8;
+                        const bool in = row < args.M && col < args.out;
+                        EpiOperands op;
+                        if (in) op.load(args.epi, row, args.out, col);
+                        float4 p0 = {}, p1 = {};
+                        if (add_partial) {
+                            const float4 *pv = reinterpret_cast<const float4 *>(pp + (c8 >> 2) * (128 * 32) + (c8 & 3) * 8);
+                            p0 = pv[0];
+                            p1 = pv[1];
+                        }
+                        uint32_t v[8];
+                        tmem_ld_32x32b_x8(tmem_base + ((q * 32) << 16) + ab * BN + c8 * 8, v);
+                        tmem_ld_wait();
+                        if (in) {
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[e]);
+                            if (add_partial) {
+                                f[0] += p0.x; f[1] += p0.y; f[2] += p0.z; f[3] += p0.w;
+                                f[4] += p1.x; f[5] += p1.y; f[6] += p1.z; f[7] += p1.w;
+                            }
+                            const int64_t o = static_cast<int64_t>(row) * args.out + col;
+                            epilogue8(args.epi, op, o, f);
+                            *reinterpret_cast<uint4 *>(args.D + o) = bf16_pack8(f);
+                        }
+                    }
+                } else {
                 uint16_t *drow = args.D + static_cast<int64_t>(row) * args.out;
 #pragma unroll 1
                 for (int c2 = 0; c2 < 2 * kChunks; ++c2) {      // 16 columns at a time
@@ -543,7 +574,6 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
                                     f4[1] = make_float4(f[4], f[5], f[6], f[7]);
                                     continue;
                                 }
-                                if constexpr (EPI) epilogue8(args.epi, row, args.out, col, f);
                                 uint32_t p[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
@@ -555,6 +585,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
                             }
                         }
                     }
+                }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -686,7 +717,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
                 *reinterpret_cast<uint4 *>(brow + ((c ^ swz) << 4)) = make_uint4(w0, w1, w2, w3);
             };
             if (main) {
-                const BlockLut L = EPI && (cur.it & ps) ? make_block_lut_rest(s) : make_block_lut(s);
+                const BlockLut L = TWICE && (cur.it & ps) ? make_block_lut_rest(s) : make_block_lut(s);
                 const uint32_t words[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
 #pragma unroll
                 for (int wd = 0; wd < 8; ++wd) {

@@ -511,7 +511,6 @@ nf4_status launch_gemm_pair(const nf4_weight *w, const uint16_t *act, int64_t M,
     a.D = D;
     a.D32 = D32;
     if (epi) a.epi = *epi;
-    a.twice = twice ? 1 : 0;
 
     const int dev = current_device();
     const int cap = pair_capacity<BN, DGRAD, G>(dev);
@@ -534,7 +533,8 @@ nf4_status launch_gemm_pair(const nf4_weight *w, const uint16_t *act, int64_t M,
         if (D32) kern = qlora_gemm_pair_kernel<BN, DGRAD, G, true>;
     } else {
         if (D32) return NF4_ERR_INVALID_ARG;      // the fp32 result is a dgrad form
-        if (epi) kern = qlora_gemm_pair_kernel<BN, DGRAD, G, false, true>;
+        if (epi) kern = twice ? qlora_gemm_pair_kernel<BN, DGRAD, G, false, true, true>
+                              : qlora_gemm_pair_kernel<BN, DGRAD, G, false, true, false>;
     }
     if (D32 || epi)      // pair_capacity has set the plain form's attribute
         NF4_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes));
