@@ -146,45 +146,6 @@ __device__ __forceinline__ void bf16_unpack8(const uint4 &v, float (&f)[8]) {
     f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
 }
 
-__device__ __forceinline__ void prefetch_l2(const void *p) {
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
-// The output step on eight consecutive columns [col, col + 8) of one row: its
-// operands, then f from the fp32 sum to h. mul and residual may be the output
-// itself: the thread that reads an element is the one that then writes it, so
-// these are plain loads.
-struct EpiOperands {
-    uint4 bias, mul, residual;
-    __device__ __forceinline__ void load(const EpiArgs &e, int row, int N, int col) {
-        const int64_t o = static_cast<int64_t>(row) * N + col;
-        if (e.mul) mul = *reinterpret_cast<const uint4 *>(e.mul + o);
-        if (e.residual) residual = *reinterpret_cast<const uint4 *>(e.residual + o);
-        if (e.bias) bias = __ldg(reinterpret_cast<const uint4 *>(e.bias + col));
-    }
-};
-
-__device__ __forceinline__ void epilogue8(const EpiArgs &e, const EpiOperands &op, int64_t o, float (&f)[8]) {
-    float v[8];
-    if (e.bias) {
-        bf16_unpack8(op.bias, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += v[i];
-    }
-    if (e.z) *reinterpret_cast<uint4 *>(e.z + o) = bf16_pack8(f);
-    act8(f, e.act);
-    if (e.mul) {
-        bf16_unpack8(op.mul, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= v[i];
-    }
-    if (e.residual) {
-        bf16_unpack8(op.residual, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += v[i];
-    }
-}
-
 // ---------------------------------------------------------------------------
 // dz = dH . mul . act'(z) (bf16, the operand of the backward's products),
 // dmul = dH . act(z), dbias = sum over tokens of dz (summed in fp32 before the

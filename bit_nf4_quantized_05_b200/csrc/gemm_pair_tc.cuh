@@ -40,6 +40,8 @@
 // taking every G-th stage).
 #pragma once
 
+#include <type_traits>
+
 #include "epilogue.cuh"
 
 namespace nf4 {
@@ -80,7 +82,21 @@ struct GemmArgs {
     EpiArgs epi;        // the output step of the EPI instantiations
 };
 
-template <int BN, bool DGRAD, int G>
+// Output step of the EPI instantiations. Each epilogue warp has its own buffers
+// for its 32 rows x 32 columns at a time: two slots for mul and residual, filled
+// by TMA ahead of use, and one from which z and h are stored by TMA. (An output
+// thread owns a row. Reading its operands itself, 16 bytes from each of 32 rows
+// per instruction, kept the load pipe from the dequantisation warps: residual
+// alone cost 19% of the 28672 x 8192 forward at 4096 tokens.)
+constexpr int kEpiTile = 32 * 32 * 2;
+constexpr int kEpiWarpBytes = 5 * kEpiTile;       // mul and residual twice, output
+
+struct alignas(64) EpiMaps {
+    CUtensorMap h, z, mul, residual;              // [M, out] bf16, box {32, 32}, 64-byte swizzle
+};
+struct NoEpiMaps {};
+
+template <int BN, bool DGRAD, int G, bool EPI = false>
 struct PairCfg {
     static constexpr int kBH = BN / 2;                    // B columns held by one CTA
     static constexpr int kABytes = kBM * kBK * 2;         // 16 KB
@@ -88,13 +104,14 @@ struct PairCfg {
     static constexpr int kCBytes = kBH * kBK / 2;         // its 4-bit codes
     static constexpr int kSB = G >= 4 ? G : 2 * G;       // weight-tile stages
     static constexpr int kSC = G >= 4 ? G : 2 * G;       // code-tile stages
-    static constexpr int kSAFit = (220 * 1024 - kSB * kBBytes - kSC * kCBytes) / kABytes;
+    static constexpr int kEBytes = EPI ? 4 * kEpiWarpBytes : 0;
+    static constexpr int kSAFit = ((EPI ? 225 : 220) * 1024 - kSB * kBBytes - kSC * kCBytes - kEBytes) / kABytes;
     static constexpr int kSA = kSAFit > 8 ? 8 : kSAFit;
     static constexpr int kGroupWarps = kBH / 32;
     static constexpr int kThreads = 32 * (kDequantWarp0 + G * kGroupWarps);
     static constexpr int kTmemCols = (2 * BN <= 256) ? 256 : 512;
     static constexpr int kSmemBytes =
-        kSA * kABytes + kSB * kBBytes + kSC * kCBytes + 1024 /*align*/ + 512 /*barriers*/;
+        kSA * kABytes + kSB * kBBytes + kSC * kCBytes + kEBytes + 1024 /*align*/ + 512 /*barriers*/;
     static constexpr uint32_t kIdesc = idesc_bf16_f32(2 * kBM, BN, 0, DGRAD ? 1 : 0);
     static_assert(BN % 16 == 0 && BN >= 64 && BN <= 256, "pair MMA N");
     static_assert(kBH % 32 == 0, "whole dequant warps");
@@ -112,8 +129,9 @@ struct PairCfg {
     // waited for already when R >= G (the dequant group's previous stage).
     static_assert(kConsumedBars > kSA && kConsumedBars > kSB && kConsumedBars >= G,
                   "stage-consumed ring deeper than either operand ring");
-    // barriers, then the TMEM address, the abort flag and three progress counters
-    static_assert((kSA + kConsumedBars + 2 * kSC + kSB + 2 + 2 + 1) * 8 + 4 + 4 + 12 <= 512,
+    // barriers (with the output step's), then the TMEM address, the abort flag and
+    // three progress counters
+    static_assert((kSA + kConsumedBars + 2 * kSC + kSB + 2 + 2 + 1 + (EPI ? 8 : 0)) * 8 + 4 + 4 + 12 <= 512,
                   "barrier area");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
@@ -245,10 +263,7 @@ __device__ __forceinline__ void set_flag_gpu(int *flag) {
 // OUT32: the result is written in fp32 to args.D32 (for a later kernel that
 // adds to it and rounds once) instead of bf16 to args.D.
 // EPI: the output step applies args.epi (bias, activation, mul, residual) to
-// the fp32 sum before it is rounded. mul and residual rows are requested into
-// L2 while the tile's products still run: an output thread reads 32 bytes of
-// its row per 16 columns, and sixteen such reads from HBM in a row would take
-// longer than the tile.
+// the fp32 sum before it is rounded.
 // TWICE: each reduction step is followed by a second one on the
 // same activations with the rest of the weight, bf16(w - bf16(w)), and each
 // adapter step by one with the rest of the rank-r activations, so that the sum
@@ -257,12 +272,13 @@ __device__ __forceinline__ void set_flag_gpu(int *flag) {
 // elements, and each of those is wrong by its whole size (at 5120 x 5120, one
 // pass left dX 3.2% off in the 2-norm, two leave it at its output's rounding).
 template <int BN, bool DGRAD, int G, bool OUT32, bool EPI = false, bool TWICE = false>
-__global__ void __launch_bounds__(PairCfg<BN, DGRAD, G>::kThreads, 1)
+__global__ void __launch_bounds__(PairCfg<BN, DGRAD, G, EPI>::kThreads, 1)
 qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red] bf16, box {64,128}
                        const __grid_constant__ CUtensorMap tm_codes,  // [Nw, K/2] u8, box {32, rows}
                        const __grid_constant__ CUtensorMap tm_la,     // [M, r] bf16, box {64,128}
+                       const __grid_constant__ std::conditional_t<EPI, EpiMaps, NoEpiMaps> maps,
                        const GemmArgs args) {
-    using Cfg = PairCfg<BN, DGRAD, G>;
+    using Cfg = PairCfg<BN, DGRAD, G, EPI>;
     constexpr int SA = Cfg::kSA, SB = Cfg::kSB, SC = Cfg::kSC, BH = Cfg::kBH;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -270,7 +286,8 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
     uint8_t *slot_a = smem;                              // [SA][kABytes]
     uint8_t *slot_b = slot_a + SA * Cfg::kABytes;        // [SB][kBBytes]
     uint8_t *slot_c = slot_b + SB * Cfg::kBBytes;        // [SC][kCBytes]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(slot_c + SC * Cfg::kCBytes);
+    uint8_t *epi_buf = slot_c + SC * Cfg::kCBytes;       // [4][kEpiWarpBytes]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(epi_buf + Cfg::kEBytes);
     uint64_t *a_full = bars;                 // even CTA: both loads landed (1 + tx)
     uint64_t *consumed = a_full + SA;        // [kConsumedBars] MMAs of a stage done (pair commit)
     uint64_t *c_full = consumed + kConsumedBars;   // code TMA landed (1 + tx) or LoRA stage (1)
@@ -279,7 +296,8 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
     uint64_t *acc_full = b_full + SB;        // [2] accumulator complete (pair commit)
     uint64_t *acc_empty = acc_full + 2;      // [2] even CTA: drained (epilogue warps of both)
     uint64_t *mma_drain = acc_empty + 2;     // even CTA: the MMAs issued before giving up completed
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_drain + 1);
+    uint64_t *epi_full = mma_drain + 1;      // EPI: [4 warps][2] operand tiles landed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(epi_full + (EPI ? 8 : 0));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     // even CTA, read only after giving up: activation stages issued by each
     // CTA's producer, and stages the MMA issuer consumed
@@ -305,6 +323,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
             mbar_init(&acc_empty[b], 8);
         }
         mbar_init(mma_drain, 1);
+        for (int b = 0; b < (EPI ? 8 : 0); ++b) mbar_init(&epi_full[b], 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_act);
@@ -338,6 +357,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
     PairSeg sg;
     // progress of the producers and of the MMA issuer (read after giving up)
     int na = 0, nc = 0, cm = 0;
+    int ne = 0, ne_used = 0;   // EPI: this warp's operand tiles requested and used
 
     if (warp == kTmaAWarp) {
         // ------------------------------------------------ TMA: activations
@@ -459,17 +479,28 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
             const bool tail = sg.k0 > 0;
             const bool head = !tail && sg.k1 < nsteps;
             const int rloc = q * 32 + lane;               // row within this CTA's 128
-            if constexpr (EPI) {
-                if (!tail && m0 + rloc < args.M) {
-                    const int64_t o = static_cast<int64_t>(m0 + rloc) * args.out + n0;
-#pragma unroll
-                    for (int c = 0; c < BN; c += 64)       // 128 bytes
-                        if (n0 + c < args.out) {
-                            if (args.epi.mul) prefetch_l2(args.epi.mul + o + c);
-                            if (args.epi.residual) prefetch_l2(args.epi.residual + o + c);
-                        }
+            // EPI: the columns of this warp's rows, 32 at a time; their operands are
+            // requested two steps ahead, the first ones before the sums are complete
+            [[maybe_unused]] uint8_t *ebuf = epi_buf + q * kEpiWarpBytes;
+            [[maybe_unused]] const int esteps =
+                tail || m0 + q * 32 >= args.M ? 0 : (min(BN, args.out - n0) + 31) / 32;
+            [[maybe_unused]] auto efetch = [&](int c) {
+                if constexpr (EPI) {
+                    const uint32_t bytes = (args.epi.mul ? kEpiTile : 0) + (args.epi.residual ? kEpiTile : 0);
+                    if (c >= esteps || bytes == 0) return;
+                    if (lane == 0) {
+                        uint64_t *bar = &epi_full[2 * q + (ne & 1)];
+                        uint8_t *dst = ebuf + (ne & 1) * 2 * kEpiTile;
+                        mbar_arrive_expect_tx(bar, bytes);
+                        if (args.epi.mul) tma_load_2d(dst, &maps.mul, bar, n0 + c * 32, m0 + q * 32);
+                        if (args.epi.residual)
+                            tma_load_2d(dst + kEpiTile, &maps.residual, bar, n0 + c * 32, m0 + q * 32);
+                    }
+                    ++ne;
                 }
-            }
+            };
+            efetch(0);
+            efetch(1);
             if (!mbar_wait(&acc_full[ab], aph, abort_flag)) goto done;
             tc_fence_after();
             if (tail) {
@@ -507,35 +538,69 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,    // [M, red
                 }
                 const int row = m0 + rloc;
                 if constexpr (EPI) {
-                    // 8 columns at a time: the operands of the output step take the
-                    // registers that the plain form spends on 16
+                    uint8_t *out = ebuf + 4 * kEpiTile;
+                    const bool ops = args.epi.mul || args.epi.residual;
+                    // 16-byte piece p of this thread's row in a 64-byte-swizzled tile
+                    auto piece = [&](uint8_t *tile, int p) {
+                        return reinterpret_cast<uint4 *>(tile + lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4));
+                    };
 #pragma unroll 1
-                    for (int c8 = 0; c8 < BN / 8; ++c8) {
-                        const int col = n0 + c8 * 8;
-                        const bool in = row < args.M && col < args.out;
-                        EpiOperands op;
-                        if (in) op.load(args.epi, row, args.out, col);
-                        float4 p0 = {}, p1 = {};
-                        if (add_partial) {
-                            const float4 *pv = reinterpret_cast<const float4 *>(pp + (c8 >> 2) * (128 * 32) + (c8 & 3) * 8);
-                            p0 = pv[0];
-                            p1 = pv[1];
-                        }
-                        uint32_t v[8];
-                        tmem_ld_32x32b_x8(tmem_base + ((q * 32) << 16) + ab * BN + c8 * 8, v);
-                        tmem_ld_wait();
-                        if (in) {
-                            float f[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[e]);
-                            if (add_partial) {
-                                f[0] += p0.x; f[1] += p0.y; f[2] += p0.z; f[3] += p0.w;
-                                f[4] += p1.x; f[5] += p1.y; f[6] += p1.z; f[7] += p1.w;
+                    for (int c = 0; c < esteps; ++c) {
+                        const int col = n0 + c * 32;
+                        uint8_t *in = ebuf + (ne_used & 1) * 2 * kEpiTile;
+                        // z first (the sum is read from tensor memory again for h)
+#pragma unroll 1
+                        for (int pass = args.epi.z ? 0 : 1; pass < 2; ++pass) {
+                            if (pass == 1 && ops) {
+                                if (!mbar_wait_warp(&epi_full[2 * q + (ne_used & 1)],
+                                                    static_cast<uint32_t>(ne_used >> 1) & 1u, abort_flag))
+                                    goto done;
+                                ++ne_used;
                             }
-                            const int64_t o = static_cast<int64_t>(row) * args.out + col;
-                            epilogue8(args.epi, op, o, f);
-                            *reinterpret_cast<uint4 *>(args.D + o) = bf16_pack8(f);
+                            if (lane == 0) tma_store_wait_read();       // the output tile before has been read
+                            __syncwarp();
+#pragma unroll 1
+                            for (int p = 0; p < 4; ++p) {
+                                uint32_t v[8];
+                                tmem_ld_32x32b_x8(tmem_base + ((q * 32) << 16) + ab * BN + c * 32 + p * 8, v);
+                                float f[8], w[8];
+                                uint4 b4 = make_uint4(0, 0, 0, 0);
+                                if (args.epi.bias && col + p * 8 < args.out)
+                                    b4 = __ldg(reinterpret_cast<const uint4 *>(args.epi.bias + col + p * 8));
+                                bf16_unpack8(b4, w);
+                                if (add_partial) {
+                                    const float4 *pv =
+                                        reinterpret_cast<const float4 *>(pp + c * (128 * 32) + p * 8);
+                                    const float4 p0 = pv[0], p1 = pv[1];
+                                    w[0] += p0.x; w[1] += p0.y; w[2] += p0.z; w[3] += p0.w;
+                                    w[4] += p1.x; w[5] += p1.y; w[6] += p1.z; w[7] += p1.w;
+                                }
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[e]) + w[e];
+                                if (pass == 1) {
+                                    act8(f, args.epi.act);
+                                    if (args.epi.mul) {
+                                        bf16_unpack8(*piece(in, p), w);
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e) f[e] *= w[e];
+                                    }
+                                    if (args.epi.residual) {
+                                        bf16_unpack8(*piece(in + kEpiTile, p), w);
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e) f[e] += w[e];
+                                    }
+                                }
+                                *piece(out, p) = bf16_pack8(f);
+                            }
+                            fence_proxy_async_smem();    // the tile's writes (and the operands' reads) before the copies
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_2d(pass == 0 ? &maps.z : &maps.h, out, col, m0 + q * 32);
+                                tma_store_commit();
+                            }
                         }
+                        efetch(c + 2);
                     }
                 } else {
                 uint16_t *drow = args.D + static_cast<int64_t>(row) * args.out;
@@ -800,6 +865,14 @@ done:
         } else {
             const uint32_t dst = mapa_shared(smem_u32(const_cast<int *>(progress)) + 4u, 0u);
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst), "r"(na) : "memory");
+        }
+    }
+    if constexpr (EPI) {
+        if (warp < kEpiWarp0 + 4 && lane == 0) {
+            tma_store_wait_all();
+            // operand tiles still on the way (after giving up)
+            for (int i = ne_used; i < ne; ++i)
+                mbar_drain(&epi_full[2 * warp + (i & 1)], static_cast<uint32_t>(i >> 1) & 1u);
         }
     }
     if (lane == 0 && warp == kTmaCWarp) {

@@ -528,19 +528,41 @@ nf4_status launch_gemm_pair(const nf4_weight *w, const uint16_t *act, int64_t M,
         a.partial = sk->partial;
         a.flags = sk->flags;
     }
+    const dim3 grid(static_cast<unsigned>(2 * pairs)), block(Cfg::kThreads);
+    if constexpr (!DGRAD) {
+        if (D32) return NF4_ERR_INVALID_ARG;      // the fp32 result is a dgrad form
+        if (epi) {
+            using ECfg = PairCfg<BN, DGRAD, G, true>;
+            EpiMaps maps;
+            auto out_map = [&](CUtensorMap *m, const uint16_t *t) {
+                return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, t ? t : D, out, M, 32, 32,
+                                CU_TENSOR_MAP_SWIZZLE_64B);
+            };
+            if (!out_map(&maps.h, D) || !out_map(&maps.z, epi->z) || !out_map(&maps.mul, epi->mul) ||
+                !out_map(&maps.residual, epi->residual))
+                return map_fail(__LINE__);
+            auto kern = twice ? qlora_gemm_pair_kernel<BN, DGRAD, G, false, true, true>
+                              : qlora_gemm_pair_kernel<BN, DGRAD, G, false, true, false>;
+            NF4_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ECfg::kSmemBytes));
+            LaunchTimer t(KK_GEMM_FWD, stream);
+            const cudaError_t e = launch_ex(kern, grid, block, ECfg::kSmemBytes, stream, 2u, tm_act, tm_codes, tm_la,
+                                            maps, a);
+            t.stop();
+            if (e != cudaSuccess) return cuda_fail(e, __LINE__);
+            NF4_TRY_CUDA(cudaGetLastError());
+            return NF4_OK;
+        }
+    }
     auto kern = qlora_gemm_pair_kernel<BN, DGRAD, G, false>;
     if constexpr (DGRAD) {
-        if (D32) kern = qlora_gemm_pair_kernel<BN, DGRAD, G, true>;
-    } else {
-        if (D32) return NF4_ERR_INVALID_ARG;      // the fp32 result is a dgrad form
-        if (epi) kern = twice ? qlora_gemm_pair_kernel<BN, DGRAD, G, false, true, true>
-                              : qlora_gemm_pair_kernel<BN, DGRAD, G, false, true, false>;
+        if (D32) {                                // (pair_capacity has set the plain form's attribute)
+            kern = qlora_gemm_pair_kernel<BN, DGRAD, G, true>;
+            NF4_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes));
+        }
     }
-    if (D32 || epi)      // pair_capacity has set the plain form's attribute
-        NF4_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes));
     LaunchTimer t(DGRAD ? KK_GEMM_DGRAD : KK_GEMM_FWD, stream);
-    const cudaError_t e = launch_ex(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::kThreads),
-                                    Cfg::kSmemBytes, stream, 2u, tm_act, tm_codes, tm_la, a);
+    const cudaError_t e =
+        launch_ex(kern, grid, block, Cfg::kSmemBytes, stream, 2u, tm_act, tm_codes, tm_la, NoEpiMaps{}, a);
     t.stop();
     if (e != cudaSuccess) return cuda_fail(e, __LINE__);
     NF4_TRY_CUDA(cudaGetLastError());
