@@ -214,10 +214,10 @@ class QuantizedWeight:
 
     def struct(self) -> NF4WeightStruct:
         self._check_arrays()
-        return NF4WeightStruct(self.n, self.k, self.block_size, int(self.double_quant),
-                               self.codes.data_ptr(), self.absmax.data_ptr(),
-                               self.absmax_q8.data_ptr() if self.absmax_q8 is not None else None,
-                               self.absmax_c.data_ptr() if self.absmax_c is not None else None)
+        codes, q8, c = self.codes, self.absmax_q8, self.absmax_c
+        return NF4WeightStruct(self.n, self.k, self.block_size, self.double_quant, codes.data_ptr(),
+                               self.absmax.data_ptr(), None if q8 is None else q8.data_ptr(),
+                               None if c is None else c.data_ptr())
 
     @property
     def device(self) -> torch.device:

@@ -141,6 +141,13 @@ __global__ void __launch_bounds__(kMrThreads)
 nf4_moe_router_kernel(const MoeArgs a) {
     constexpr int kOut = kMrTokens * kMrExperts;
     __shared__ double part[kMrThreads / 32][kOut];
+    {
+        // on the way into L2 while the kernel before finishes
+        const int e = static_cast<int>(blockIdx.x) * kMrExperts + (threadIdx.x >> 5);
+        const int k = static_cast<int>(blockIdx.z) * kMrSplit + (threadIdx.x & 31) * 32;
+        if (e < a.E && k < a.H)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.router + static_cast<int64_t>(e) * a.H + k));
+    }
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
@@ -277,22 +284,38 @@ __device__ __forceinline__ void moe_route(const MoeArgs &a, MoeHeader *h, uint8_
         }
         double mine = top;
         int my_id = 0;
+        // top_k rounds: each lane holds the best of its experts that are left (the
+        // first of equal ones); high words that differ settle a round
+        int bi = lane;
+        unsigned long long b = 0;
 #pragma unroll 1
-        for (int j = 0; j < a.top_k; ++j) {
-            unsigned long long b = 0;
-            int bi = 0;
-#pragma unroll 1
-            for (int e = lane; e < a.E; e += 32)
-                if (key(e) > b) {
-                    b = key(e);
-                    bi = e;
+        for (int j = -1; j < a.top_k; ++j) {
+            int win = lane;
+            if (j >= 0) {
+                const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(b >> 32));
+                uint32_t tied = __ballot_sync(0xffffffffu, static_cast<uint32_t>(b >> 32) == hi);
+                if (tied & (tied - 1)) {
+                    const unsigned long long m1 = warp_max(b);
+                    const uint32_t first = __reduce_min_sync(0xffffffffu, b == m1 ? static_cast<uint32_t>(bi) : 0xffffu);
+                    tied = __ballot_sync(0xffffffffu, b == m1 && static_cast<uint32_t>(bi) == first);
                 }
-            const unsigned long long m1 = warp_max(b);
-            const int win = static_cast<int>(__reduce_min_sync(0xffffffffu, b == m1 ? static_cast<uint32_t>(bi) : 0xffffu));
-            if ((win & 31) == lane) key(win) = 0;
-            if (lane == j) {
-                my_id = win;
-                mine = key_value(m1);
+                const int from = __ffs(static_cast<int>(tied)) - 1;
+                win = __shfl_sync(0xffffffffu, bi, from);
+                const unsigned long long m1 = __shfl_sync(0xffffffffu, b, from);
+                if (lane == j) {
+                    my_id = win;
+                    mine = key_value(m1);
+                }
+                if (lane == from) key(win) = 0;
+            }
+            if ((win & 31) == lane) {                 // at first every lane, then the winner's
+                b = 0;
+#pragma unroll 1
+                for (int e = lane; e < a.E; e += 32)
+                    if (key(e) > b) {
+                        b = key(e);
+                        bi = e;
+                    }
             }
         }
         const float ex = lane < a.top_k ? expf(static_cast<float>(mine - top)) : 0.0f;
