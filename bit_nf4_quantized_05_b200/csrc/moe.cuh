@@ -214,6 +214,7 @@ struct MoeHeader {
     int nchunks;
     int last[kMoeWarps], ready[kMoeWarps];        // by group
     uint32_t claim[kMoeWarps][4];                 // by group: its items, a ring of four
+    int start[kMoeWarps][2];                      // by group: its first two, as taken
     int warp_slots[kMoeMaxExperts / 32], warp_chunks[kMoeMaxExperts / 32];
     MoeChunk chunk[kMoeMaxChunks];
     float weight[kMoeMaxSlots];                   // by slot
@@ -224,6 +225,7 @@ struct MoeHeader {
     uint8_t token[kMoeMaxSlots];                  // by slot
     uint16_t slot0[kMoeMaxExperts];
 };
+static_assert(kMoeMaxExperts * 12 <= kMoeSlotBytes, "keys and their high words in a ring slot");
 static_assert(kMoeMaxExperts <= 256 && kMoeMaxTokens <= 64, "ids in a byte, tokens in a 64-bit mask");
 constexpr int kMoeHeaderBytes = (sizeof(MoeHeader) + 1023) / 1024 * 1024;
 static_assert(kMoeHeaderBytes <= 20 * 1024, "header");
@@ -238,94 +240,72 @@ __device__ __forceinline__ double key_value(unsigned long long key) {
     return __longlong_as_double(static_cast<long long>(b >> 63 ? b & ~(1ull << 63) : ~b));
 }
 
-// The largest key of the warp.
-__device__ __forceinline__ unsigned long long warp_max(unsigned long long key) {
-    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32));
-    const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32) == hi ? static_cast<uint32_t>(key) : 0u);
-    return static_cast<unsigned long long>(hi) << 32 | lo;
-}
-
 // Routing of all tokens, by every thread of the CTA: the chosen experts with
 // their weights, the chunks, and the slots. Larger logit first, ties to the
 // lower index; a NaN counts as minus infinity (its weights are NaN all the same).
-// A warp takes a token, with the experts' keys in the odd halves of 16 table
-// rows. The loops stay rolled: this runs once a launch, and fetching the
-// instructions of an unrolled form took most of its 4 us.
-__device__ __forceinline__ void moe_route(const MoeArgs &a, MoeHeader *h, uint8_t *table) {
+// A warp takes a token. A lane counts, for each of its experts, the keys above:
+// by their high words, and by whole keys only where two of those are equal
+// (rounds of a warp maximum took three times as long at 8 of 64 experts). The
+// keys are where the warp's ring slots will be: kMoeMaxExperts of them, then
+// their high words.
+__device__ __forceinline__ void moe_route(const MoeArgs &a, MoeHeader *h, unsigned long long *key) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < kMoeMaxExperts; e += kMoeThreads) h->mask[e] = 0;
     __syncthreads();
-    // expert e's key; 0 once it is taken
-    auto key = [&](int e) -> unsigned long long & {
-        return *reinterpret_cast<unsigned long long *>(table + (warp * 16 + (e >> 4)) * 256 + 128 + (e & 15) * 8);
-    };
+    uint32_t *high = reinterpret_cast<uint32_t *>(key + kMoeMaxExperts);
     const int64_t split = static_cast<int64_t>(a.M) * a.E;
 #pragma unroll 1
     for (int m = warp; m < a.M; m += kMoeThreads / 32) {
         bool nan = false;
-        unsigned long long best = 0;
 #pragma unroll 1
-        for (int e = lane; e < a.E; e += 32) {
+        for (int e = lane; e < ((a.E + 3) & ~3); e += 32) {
             const double *l = a.logits + static_cast<int64_t>(m) * a.E + e;
             double v = 0.0;
+            if (e < a.E) {
 #pragma unroll 4
-            for (int s = 0; s < a.splits; ++s) v += __ldcg(l + s * split);
+                for (int s = 0; s < a.splits; ++s) v += __ldcg(l + s * split);
+            }
             nan |= isnan(v);
-            key(e) = order_key(v);
-            best = max(best, key(e));
+            key[e] = e < a.E ? order_key(v) : 0ull;
+            high[e] = static_cast<uint32_t>(key[e] >> 32);
         }
         nan = __any_sync(0xffffffffu, nan) != 0;
-        const double top = key_value(warp_max(best));
+        __syncwarp();
+#pragma unroll 1
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = min(e0 + lane, a.E - 1);
+            const uint32_t mine = high[e];
+            int rank = 0, same = 0;
+#pragma unroll 2
+            for (int f = 0; f < a.E; f += 4) {
+                const uint4 h4 = *reinterpret_cast<const uint4 *>(high + f);
+                rank += (h4.x > mine) + (h4.y > mine) + (h4.z > mine) + (h4.w > mine);
+                same += (h4.x == mine) + (h4.y == mine) + (h4.z == mine) + (h4.w == mine);
+            }
+            if (__any_sync(0xffffffffu, same > 1)) {
+                rank = 0;
+#pragma unroll 1
+                for (int f = 0; f < a.E; ++f) rank += key[f] > key[e] || (key[f] == key[e] && f < e) ? 1 : 0;
+            }
+            if (e0 + lane < a.E && rank < a.top_k) h->id[m * a.top_k + rank] = static_cast<uint8_t>(e);
+        }
+        __syncwarp();
+        const int my_id = h->id[m * a.top_k + min(lane, a.top_k - 1)];
+        const double top = key_value(key[h->id[m * a.top_k]]);
         // (infinities propagate through the sum as in a softmax)
+        const float ex = lane < a.top_k ? expf(static_cast<float>(key_value(key[my_id]) - top)) : 0.0f;
         float sum = 0.0f;
-        if (!a.renorm) {
+        if (a.renorm) {
+            sum = ex;
+        } else {
 #pragma unroll 1
-            for (int e = lane; e < a.E; e += 32) sum += expf(static_cast<float>(key_value(key(e)) - top));
+            for (int e = lane; e < a.E; e += 32) sum += expf(static_cast<float>(key_value(key[e]) - top));
         }
-        double mine = top;
-        int my_id = 0;
-        // top_k rounds: each lane holds the best of its experts that are left (the
-        // first of equal ones); high words that differ settle a round
-        int bi = lane;
-        unsigned long long b = 0;
-#pragma unroll 1
-        for (int j = -1; j < a.top_k; ++j) {
-            int win = lane;
-            if (j >= 0) {
-                const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(b >> 32));
-                uint32_t tied = __ballot_sync(0xffffffffu, static_cast<uint32_t>(b >> 32) == hi);
-                if (tied & (tied - 1)) {
-                    const unsigned long long m1 = warp_max(b);
-                    const uint32_t first = __reduce_min_sync(0xffffffffu, b == m1 ? static_cast<uint32_t>(bi) : 0xffffu);
-                    tied = __ballot_sync(0xffffffffu, b == m1 && static_cast<uint32_t>(bi) == first);
-                }
-                const int from = __ffs(static_cast<int>(tied)) - 1;
-                win = __shfl_sync(0xffffffffu, bi, from);
-                const unsigned long long m1 = __shfl_sync(0xffffffffu, b, from);
-                if (lane == j) {
-                    my_id = win;
-                    mine = key_value(m1);
-                }
-                if (lane == from) key(win) = 0;
-            }
-            if ((win & 31) == lane) {                 // at first every lane, then the winner's
-                b = 0;
-#pragma unroll 1
-                for (int e = lane; e < a.E; e += 32)
-                    if (key(e) > b) {
-                        b = key(e);
-                        bi = e;
-                    }
-            }
-        }
-        const float ex = lane < a.top_k ? expf(static_cast<float>(mine - top)) : 0.0f;
-        if (a.renorm) sum = ex;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane < a.top_k) {
             const float w = nan ? __int_as_float(0x7fffffff) : ex / sum;
             const int i = m * a.top_k + lane;
-            h->id[i] = static_cast<uint8_t>(my_id);
             h->w[i] = w;
             atomicOr(&h->mask[my_id], 1ull << m);
             if (blockIdx.x == 0) {
@@ -406,6 +386,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate_up,   // u8 [2 E, F, H/2], box {64, 32, 2}, 64-byte swizzle
                        const __grid_constant__ CUtensorMap tm_down,      // u8 [E H, F/2], box {64, 64}, 64-byte swizzle
                        const MoeArgs a) {
+    constexpr int kGroups = kMoeWarps / GW;
+    static_assert(kGroups * GW == kMoeWarps, "a group's barrier counts its warps");
     extern __shared__ __align__(1024) uint8_t dsm[];
     const uint32_t sbase = smem_u32(dsm);
     const uint32_t low0 = (sbase + kMoeHeaderBytes + 1023u) & ~1023u;
@@ -439,14 +421,26 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate_up,   // u8 [
     griddep_wait();
     griddep_launch_dependents();
 
+    uint32_t slot[kMoeRing];
+#pragma unroll
+    for (int s = 0; s < kMoeRing; ++s) {
+        const uint32_t i = static_cast<uint32_t>(warp * kMoeRing + s);
+        slot[s] = i < nlow ? low0 + i * kMoeSlotBytes : kDsHighAddr + (i - nlow) * kMoeSlotBytes;
+    }
+
     // ---- items are taken by the group's first thread, two ahead of the one
     // being computed: the last step of an item already requests the next one's
-    // data, and the atomic of the one after it is in flight meanwhile. At the
-    // start a group takes one at a time, so that few items spread over the grid.
+    // data, and the atomic of the one after it is in flight meanwhile. The first
+    // two are taken by the last warp, which has the fewest tokens to route, one
+    // after the other, so that few items spread over the grid.
     const bool taker = gw == 0 && lane == 0;
     int taken = 0;
-    if (taker) taken = atomicAdd(&a.cnt->claimed, 1);
-    moe_route(a, hd, lut_g);
+    if (warp == kMoeWarps - 1 && lane < kGroups) {
+        const int c0 = atomicAdd(&a.cnt->claimed, 1);
+        hd->start[lane][0] = c0;
+        hd->start[lane][1] = atomicAdd(&a.cnt->claimed, c0 < 0 ? 0 : 1);
+    }
+    moe_route(a, hd, reinterpret_cast<unsigned long long *>(dsm + (slot[0] - sbase)));
     __syncthreads();
     const int nchunks = hd->nchunks;
     const int tiles_gu = a.F / (kMoeRows / 2), tiles_dn = a.H / kMoeRows;
@@ -460,19 +454,14 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate_up,   // u8 [
         return (dn ? 1u << 31 : 0u) | static_cast<uint32_t>(c) << 22 | static_cast<uint32_t>(i - c * per);
     };
     if (taker) {
-        hd->claim[grp][0] = item_of(taken);
+        hd->claim[grp][0] = item_of(hd->start[grp][0]);
+        hd->claim[grp][1] = item_of(hd->start[grp][1]);
         taken = atomicAdd(&a.cnt->claimed, 1);
     }
     group_sync<32 * GW>(grp);
     int seq = 0;                                               // the current item is claim[seq % 4]
     uint32_t cur = hd->claim[grp][0];
 
-    uint32_t slot[kMoeRing];
-#pragma unroll
-    for (int s = 0; s < kMoeRing; ++s) {
-        const uint32_t i = static_cast<uint32_t>(warp * kMoeRing + s);
-        slot[s] = i < nlow ? low0 + i * kMoeSlotBytes : kDsHighAddr + (i - nlow) * kMoeSlotBytes;
-    }
     int issued = 0, landed = 0;
     // request one step's codes (kc-th 128 elements of the item's 64 rows)
     auto issue = [&](uint32_t it, int kc) {
@@ -507,12 +496,6 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate_up,   // u8 [
     };
 
     if (cur != kMoeNoItem) issue(cur, first_step(item_down(cur)));
-    if (taker) {
-        hd->claim[grp][1] = item_of(taken);
-        taken = atomicAdd(&a.cnt->claimed, 1);
-    }
-    group_sync<32 * GW>(grp);
-
     // ---- the items of one kind, to the group's last of them
     auto run = [&](auto down_c) {
         constexpr bool DOWN = decltype(down_c)::value;
