@@ -634,7 +634,7 @@ def qlora_linear_fwd_epilogue(qw: QuantizedWeight, x: torch.Tensor, A: torch.Ten
         if workspace is None:
             workspace = _workspace(fwd_epilogue_workspace_bytes(M, qw.n, qw.k, r), x.device)
         _check(lib.qlora_linear_fwd_epilogue(ctypes.byref(qw.struct()), x.data_ptr(), M, A.data_ptr(), B.data_ptr(),
-                                             r, alpha, ctypes.byref(ep), h.data_ptr(), _addr(z), _addr(u),
+                                             r, float(alpha), ctypes.byref(ep), h.data_ptr(), _addr(z), _addr(u),
                                              workspace.data_ptr(), workspace.numel(), _raw_stream(dev)),
                "qlora_linear_fwd_epilogue")
     return h, u, z
@@ -679,7 +679,7 @@ def qlora_linear_bwd_epilogue(qw: QuantizedWeight, x: torch.Tensor, A: torch.Ten
         if workspace is None:
             workspace = _workspace(bwd_epilogue_workspace_bytes(M, qw.n, qw.k, r), x.device)
         _check(lib.qlora_linear_bwd_epilogue(ctypes.byref(qw.struct()), x.data_ptr(), M, A.data_ptr(), B.data_ptr(),
-                                             r, alpha, ctypes.byref(ep), dH.data_ptr(), _addr(z), _addr(u),
+                                             r, float(alpha), ctypes.byref(ep), dH.data_ptr(), _addr(z), _addr(u),
                                              _addr(dX), dA.data_ptr(), dB.data_ptr(), _addr(dbias), _addr(dmul),
                                              grad_dtype is torch.float32, workspace.data_ptr(), workspace.numel(),
                                              _raw_stream(dev)), "qlora_linear_bwd_epilogue")
@@ -700,9 +700,10 @@ def nf4_moe_fwd(gate_up: QuantizedWeight, down: QuantizedWeight, x: torch.Tensor
     [E * 2 * ffn, hidden] (per expert: ffn gate rows, then ffn up rows), down
     their down rows, [E * hidden, ffn]. Returns (out [M, hidden] bf16, ids
     [M, top_k] int32, weights [M, top_k] fp32); see the C header for the routing
-    rule. out may be the residual itself."""
+    rule. out may be the residual itself, and x."""
     if x.dim() != 2 or router.dim() != 2:
         raise ValueError("x and router must be 2-D")
+    top_k = int(top_k)
     M, H, E, dev = x.shape[0], gate_up.k, router.shape[0], gate_up.codes.get_device()
     _check_fast("x", x, (M, H), torch.bfloat16, gate_up, dev)
     _check_fast("router", router, (E, H), torch.bfloat16, gate_up, dev)

@@ -245,7 +245,7 @@ __device__ __forceinline__ double key_value(unsigned long long key) {
 // lower index; a NaN counts as minus infinity (its weights are NaN all the same).
 // A warp takes a token. A lane counts, for each of its experts, the keys above:
 // by their high words, and by whole keys only where two of those are equal
-// (rounds of a warp maximum took three times as long at 8 of 64 experts). The
+// (8 rounds of a warp maximum over 64 experts took twice as long). The
 // keys are where the warp's ring slots will be: kMoeMaxExperts of them, then
 // their high words.
 __device__ __forceinline__ void moe_route(const MoeArgs &a, MoeHeader *h, unsigned long long *key) {
@@ -496,6 +496,7 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate_up,   // u8 [
     };
 
     if (cur != kMoeNoItem) issue(cur, first_step(item_down(cur)));
+
     // ---- the items of one kind, to the group's last of them
     auto run = [&](auto down_c) {
         constexpr bool DOWN = decltype(down_c)::value;
@@ -730,7 +731,7 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate_up,   // u8 [
                 const int rr = 16 * (j >> 2) + prow + 8 * (e >> 1), col = 2 * t + (e & 1);
                 if (col < c.n) {
                     if constexpr (!DOWN) {
-                        // s0 is gate row rr, s1 up row rr
+                        // s0 is gate row rr, s1 up row rr; rounded to the down product's operand
                         const __nv_bfloat16 v = __float2bfloat16_rn(act_value(s0, a.act) * s1);
                         a.a[static_cast<int64_t>(c.slot0 + col) * a.F + tile * (kMoeRows / 2) + rr] =
                             *reinterpret_cast<const uint16_t *>(&v);

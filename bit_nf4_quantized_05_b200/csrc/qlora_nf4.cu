@@ -1537,8 +1537,8 @@ nf4_status nf4_moe_fwd(const nf4_weight *gate_up, const nf4_weight *down, const 
     if (!aligned16(x) || !aligned16(router) || !aligned16(residual) || !aligned16(out) || !aligned16(topk_ids) ||
         !aligned16(topk_weights))
         return NF4_ERR_ALIGNMENT;
-    // out is written while residual is still read, an element by the thread
-    // that read it; x is not read any more by then
+    // out is written while residual is still read, an element by the thread that
+    // read it; x is not used any more by then (every gate-up item is done)
     if (residual != out && overlap(residual, out, M * H)) return NF4_ERR_INVALID_ARG;
     const MoeLayout L = moe_layout(M, E, H, F, top_k);
     if (!workspace || ws_bytes < L.total) return NF4_ERR_WORKSPACE;

@@ -354,10 +354,12 @@ QLORA_API nf4_status qlora_linear_bwd_epilogue(const nf4_weight *w, const uint16
  * up rows; down is [n_experts * hidden, ffn]; the two may differ in block size and
  * scale form. x [M, hidden], router [n_experts, hidden], residual (nullable) and
  * out [M, hidden] bf16; topk_ids [M, top_k] int32 and topk_weights [M, top_k] fp32
- * (both nullable) receive the routing. Weights enter as in the few-token
- * form of qlora_linear_fwd (the levels as bf16, each block's fp32 sum times its
- * scale); the logits are summed in fp64; act(..) . (..) is rounded to bf16; the
- * weighted sum is fp32, rounded once. out may be the residual itself.
+ * (both nullable) receive the routing. The products take a fixed multiple of the
+ * levels rounded to bf16 (0.08% of a weight in the mean square) and scale each
+ * block's fp32 sum; the logits are summed in fp64; act(..) . (..) is rounded to
+ * bf16; the weighted sum is fp32, rounded once. out may be the same buffer as
+ * residual, x or both; any other overlap of out and residual returns
+ * NF4_ERR_INVALID_ARG.
  * Requirements: 0 <= M <= 64, 1 <= n_experts <= 256, 1 <= top_k <=
  * min(16, n_experts), hidden and ffn at most 2^20, those of the weights, every
  * pointer 16-byte aligned. workspace: at least nf4_moe_workspace_bytes(M,

@@ -101,7 +101,7 @@ def check_moe(q, m, got, act, renorm, residual):
 SHAPES = [
     (1, 8, 2, 256, 128), (2, 4, 4, 64, 64), (7, 16, 3, 320, 192), (8, 5, 1, 2048, 1408), (9, 2, 2, 448, 704),
     (16, 64, 6, 512, 320), (17, 256, 16, 128, 64), (33, 3, 2, 1088, 576), (64, 32, 8, 256, 256),
-    (64, 1, 1, 128, 128), (3, 8, 2, 5120, 2112),
+    (64, 1, 1, 128, 128), (3, 8, 2, 5120, 2112), (64, 256, 16, 64, 64),
 ]
 
 
