@@ -37,8 +37,7 @@ constexpr float kGeluTanhCubic = 0.044715f;
 //   erfc(x) = t 2^(-x^2 log2(e) + Q(t)),
 // where Q is a degree-7 Chebyshev fit of log2(erfc(x) e^(x^2) / t) over
 // 0.08 <= t <= 1: 1e-6 relative, also where erfc itself is tiny (beyond |z| =
-// 32 both are 0 in fp32). One reciprocal and one exponential; erfcf took 2.5
-// times the output step's time.
+// 32 both are 0 in fp32). One reciprocal, one exponential and eight multiply-adds.
 __device__ __forceinline__ float normal_cdf(float z) {
     const float t = __fdividef(1.0f, fmaf(0.35355339059327376f, fabsf(z), 1.0f));
     float q = -0.27331653237342834f;
@@ -155,7 +154,9 @@ __device__ __forceinline__ void bf16_unpack8(const uint4 &v, float (&f)[8]) {
 // 128 columns (16 lanes of 8) and every (32 x splits)-th row from its own; the
 // splits of one column stripe are a cluster, so the column sums meet in
 // distributed shared memory and are added in a fixed order: one launch, no
-// atomics, no workspace. dz is null when there is neither activation nor mul
+// atomics, no workspace. A thread has two rows in flight. 225 us at 28672
+// columns and 4096 tokens with mul and dmul (5.2 TB/s); 30 us at 5120 columns and
+// 2048 tokens, where the grid is just over one wave. dz is null when there is neither activation nor mul
 // (then dz is dH itself and only the column sums are formed).
 // ---------------------------------------------------------------------------
 constexpr int kEbThreads = 512;

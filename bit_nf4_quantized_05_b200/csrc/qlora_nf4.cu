@@ -1308,18 +1308,17 @@ nf4_status qlora_linear_bwd_dropout_philox(const nf4_weight *w, const uint16_t *
 // ---- the layer with its epilogue
 
 // The fields of an epilogue that both directions take.
-nf4_status check_epilogue(const qlora_epilogue *ep) {
+static nf4_status check_epilogue(const qlora_epilogue *ep) {
     if (!ep || ep->act < NF4_ACT_NONE || ep->act > NF4_ACT_GELU) return NF4_ERR_INVALID_ARG;
     if (!aligned16(ep->bias) || !aligned16(ep->mul) || !aligned16(ep->residual)) return NF4_ERR_ALIGNMENT;
     return NF4_OK;
 }
 
-// Two [M, n] bf16 buffers that share some elements.
-bool overlap(const void *p, const void *q, int64_t elems) {
+// Two bf16 buffers that share some elements.
+static bool overlap(const void *p, int64_t p_elems, const void *q, int64_t q_elems) {
     if (!p || !q) return false;
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    const uintptr_t bytes = static_cast<uintptr_t>(elems) * 2;
-    return a < b + bytes && b < a + bytes;
+    return a < b + static_cast<uintptr_t>(q_elems) * 2 && b < a + static_cast<uintptr_t>(p_elems) * 2;
 }
 
 size_t qlora_fwd_epilogue_workspace_bytes(int64_t M, int64_t n, int64_t k, int32_t r) {
@@ -1338,8 +1337,9 @@ nf4_status qlora_linear_fwd_epilogue(const nf4_weight *w, const uint16_t *x, int
     if (!aligned16(z_out)) return NF4_ERR_ALIGNMENT;
     const int64_t out = M * w->n;
     // h may be mul or residual itself; z may be neither h nor an input
-    if ((h != ep->mul && overlap(h, ep->mul, out)) || (h != ep->residual && overlap(h, ep->residual, out)) ||
-        overlap(z_out, h, out) || overlap(z_out, ep->mul, out) || overlap(z_out, ep->residual, out))
+    if ((h != ep->mul && overlap(h, out, ep->mul, out)) || (h != ep->residual && overlap(h, out, ep->residual, out)) ||
+        overlap(z_out, out, h, out) || overlap(z_out, out, ep->mul, out) || overlap(z_out, out, ep->residual, out) ||
+        overlap(h, out, x, M * w->k) || overlap(z_out, out, x, M * w->k))
         return NF4_ERR_INVALID_ARG;
     const EpiArgs e{ep->act, ep->bias, ep->mul, ep->residual, z_out};
     return fwd_impl(w, x, M, A, B, r, alpha, 0.0f, nullptr, h, u_out, workspace, ws_bytes, stream, DropRng{}, &e);
@@ -1367,9 +1367,12 @@ nf4_status qlora_linear_bwd_epilogue(const nf4_weight *w, const uint16_t *x, int
     if (!aligned16(dH) || !aligned16(z) || !aligned16(u) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) ||
         !aligned16(dbias) || !aligned16(dmul))
         return NF4_ERR_ALIGNMENT;
-    // dmul is written while dH, z and mul are read
-    const int64_t out = M * w->n;
-    if (overlap(dmul, dH, out) || overlap(dmul, z, out) || overlap(dmul, ep->mul, out)) return NF4_ERR_INVALID_ARG;
+    // dmul is written while dH, z and mul are read, dX while dH (or dz) is; x is
+    // read before, but by kernels that may still run
+    const int64_t out = M * w->n, in = M * w->k;
+    if (overlap(dmul, out, dH, out) || overlap(dmul, out, z, out) || overlap(dmul, out, ep->mul, out) || overlap(dX, in, dH, out) ||
+        overlap(dX, in, dmul, out) || overlap(dX, in, x, in) || overlap(dmul, out, x, in))
+        return NF4_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t N = w->n;
     const size_t base = bwd_layout(std::max<int64_t>(M, 1), r, num_sms(current_device())).total;
@@ -1539,7 +1542,8 @@ nf4_status nf4_moe_fwd(const nf4_weight *gate_up, const nf4_weight *down, const 
         return NF4_ERR_ALIGNMENT;
     // out is written while residual is still read, an element by the thread that
     // read it; x is not used any more by then (every gate-up item is done)
-    if (residual != out && overlap(residual, out, M * H)) return NF4_ERR_INVALID_ARG;
+    if ((residual != out && overlap(residual, M * H, out, M * H)) || (x != out && overlap(x, M * H, out, M * H)))
+        return NF4_ERR_INVALID_ARG;
     const MoeLayout L = moe_layout(M, E, H, F, top_k);
     if (!workspace || ws_bytes < L.total) return NF4_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return NF4_ERR_ALIGNMENT;

@@ -307,7 +307,7 @@ typedef struct {
  * all on the fp32 sum, with one rounding to bf16 at the end. z_out (nullable,
  * [M, n] bf16) receives z for the backward. h may be the same buffer as mul or
  * residual (the residual stream updated in place); any other overlap of h or
- * z_out with mul, residual or each other returns NF4_ERR_INVALID_ARG, and so
+ * z_out with x, mul, residual or each other returns NF4_ERR_INVALID_ARG, and so
  * do a null ep and an unknown act. workspace: at least
  * qlora_fwd_epilogue_workspace_bytes(M, n, k, r) bytes, 256-byte aligned.
  * Otherwise as qlora_linear_fwd, with one difference: for a ReLU with z_out the
@@ -329,7 +329,8 @@ QLORA_API nf4_status qlora_linear_fwd_epilogue(const nf4_weight *w, const uint16
  * ep: act and mul as in the forward (bias and residual are not read). z is the
  * forward's z_out; it may be NULL when act is none and dmul is not wanted. u as
  * in qlora_linear_bwd. dX, dbias and dmul may be NULL; dmul needs ep->mul and
- * must not overlap dH, z or mul (NF4_ERR_INVALID_ARG). With grads_f32 == 1, dA, dB and dbias
+ * must not overlap dH, z, mul or x, nor dX any of dH, dmul and x
+ * (NF4_ERR_INVALID_ARG). With grads_f32 == 1, dA, dB and dbias
  * are fp32, with 0 bf16. relu'(0) = 0. workspace: at least
  * qlora_bwd_epilogue_workspace_bytes(M, n, k, r) bytes, 256-byte aligned. M == 0
  * writes zeros to dA, dB and dbias. */
@@ -358,7 +359,7 @@ QLORA_API nf4_status qlora_linear_bwd_epilogue(const nf4_weight *w, const uint16
  * levels rounded to bf16 (0.08% of a weight in the mean square) and scale each
  * block's fp32 sum; the logits are summed in fp64; act(..) . (..) is rounded to
  * bf16; the weighted sum is fp32, rounded once. out may be the same buffer as
- * residual, x or both; any other overlap of out and residual returns
+ * residual, x or both; any other overlap of out with them returns
  * NF4_ERR_INVALID_ARG.
  * Requirements: 0 <= M <= 64, 1 <= n_experts <= 256, 1 <= top_k <=
  * min(16, n_experts), hidden and ffn at most 2^20, those of the weights, every

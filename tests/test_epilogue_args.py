@@ -11,6 +11,7 @@ from epilogue_ref import act64, backward64, forward64
 N, K, M, R = 64, 128, 5, 8
 FAKE = 0x10000
 FAR = 0x4000000
+X = 0x40000000
 
 
 @pytest.fixture(scope="module")
@@ -27,7 +28,7 @@ def weight(q, n=N, k=K):
 def fwd(q, **kw):
     ep = q.EpilogueStruct(kw.get("act", 0), kw.get("bias"), kw.get("mul"), kw.get("residual"))
     return q.lib.qlora_linear_fwd_epilogue(
-        ctypes.byref(kw.get("w", weight(q))), FAKE, kw.get("M", M), FAKE, FAKE, kw.get("r", R), 16.0,
+        ctypes.byref(kw.get("w", weight(q))), X, kw.get("M", M), FAKE, FAKE, kw.get("r", R), 16.0,
         None if kw.get("no_ep") else ctypes.byref(ep), kw.get("h", FAKE), kw.get("z"), None,
         kw.get("ws", FAKE), kw.get("wsb", 16), None)
 
@@ -50,14 +51,18 @@ def test_forward_argument_checks(q):
     assert fwd(q, z=FAKE) == q.NF4_ERR_INVALID_ARG
     assert fwd(q, z=FAR, mul=FAR) == q.NF4_ERR_INVALID_ARG
     assert fwd(q, z=FAR, residual=FAR + 32) == q.NF4_ERR_INVALID_ARG
+    assert fwd(q, h=X) == q.NF4_ERR_INVALID_ARG                         # over the tokens
+    assert fwd(q, h=X + M * K * 2 - 16) == q.NF4_ERR_INVALID_ARG
+    assert fwd(q, h=X + M * K * 2) == q.NF4_ERR_WORKSPACE
+    assert fwd(q, z=X - M * N * 2 + 16) == q.NF4_ERR_INVALID_ARG
     assert fwd(q, M=0, act=2, h=None) == q.NF4_OK
 
 
 def bwd(q, **kw):
     ep = q.EpilogueStruct(kw.get("act", 0), None, kw.get("mul"), None)
     return q.lib.qlora_linear_bwd_epilogue(
-        ctypes.byref(kw.get("w", weight(q))), FAKE, kw.get("M", M), FAKE, FAKE, R, 16.0,
-        None if kw.get("no_ep") else ctypes.byref(ep), kw.get("dH", FAKE), kw.get("z"), None, None,
+        ctypes.byref(kw.get("w", weight(q))), X, kw.get("M", M), FAKE, FAKE, R, 16.0,
+        None if kw.get("no_ep") else ctypes.byref(ep), kw.get("dH", FAKE), kw.get("z"), None, kw.get("dX"),
         kw.get("dA", FAKE), FAKE, kw.get("dbias"), kw.get("dmul"), kw.get("f32", 0), kw.get("ws", FAKE),
         kw.get("wsb", 16), None)
 
@@ -70,6 +75,10 @@ def test_backward_argument_checks(q):
     assert bwd(q, z=FAKE, dmul=FAR) == q.NF4_ERR_INVALID_ARG            # dmul without mul
     assert bwd(q, z=FAR, mul=FAKE, dmul=FAKE) == q.NF4_ERR_INVALID_ARG  # dmul over its inputs
     assert bwd(q, z=FAR, mul=2 * FAR, dmul=FAR + 16) == q.NF4_ERR_INVALID_ARG
+    assert bwd(q, dX=FAKE) == q.NF4_ERR_INVALID_ARG                     # dX over dH
+    assert bwd(q, dX=X + 16) == q.NF4_ERR_INVALID_ARG
+    assert bwd(q, dX=FAR) == q.NF4_ERR_WORKSPACE
+    assert bwd(q, z=FAR, mul=2 * FAR, dmul=3 * FAR, dX=3 * FAR) == q.NF4_ERR_INVALID_ARG
     assert bwd(q, dH=None) == q.NF4_ERR_INVALID_ARG
     assert bwd(q, dA=None) == q.NF4_ERR_INVALID_ARG
     assert bwd(q, f32=2) == q.NF4_ERR_INVALID_ARG

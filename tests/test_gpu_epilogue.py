@@ -186,9 +186,9 @@ def test_extreme_pre_activations(q, M, act):
     check("dbias", dbias[fin], want[fin], tol[fin])
 
 
-@pytest.mark.parametrize("M", [9, 200])
-def test_residual_and_mul_updated_in_place(q, M):
-    c = Case(q, 520, 640, M, 16)
+@pytest.mark.parametrize("N,M", [(520, 9), (520, 200), (4104, 1100)])
+def test_residual_and_mul_updated_in_place(q, N, M):
+    c = Case(q, N, 640, M, 16)
     want, _, _ = q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.bias, "silu", c.mul, c.residual)
     for t in (c.residual.clone(), c.mul.clone()):
         kw = dict(mul=c.mul, residual=c.residual)

@@ -62,6 +62,8 @@ def test_argument_checks(q):
     assert call(q, w=FAKE + 8) == q.NF4_ERR_ALIGNMENT
     assert call(q, res=FAKE) == q.NF4_ERR_WORKSPACE                     # the residual updated in place
     assert call(q, res=FAKE + 16) == q.NF4_ERR_INVALID_ARG
+    assert call(q, x=FAKE + 16) == q.NF4_ERR_INVALID_ARG                # x half under out
+    assert call(q, x=FAKE + M * H * 2) == q.NF4_ERR_WORKSPACE
     assert call(q, gu=weight(q, E * 2 * F, H, codes=FAKE + 8)) == q.NF4_ERR_ALIGNMENT
 
 
