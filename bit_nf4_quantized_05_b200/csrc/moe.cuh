@@ -524,6 +524,7 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate_up,   // u8 [
         auto wait_chunk = [&](int chunk) -> bool {
             if (taker) {
                 const long long t0 = clock64();
+                const long long lim = g_dbg_flag_wait_limit > 0 ? g_dbg_flag_wait_limit : kWaitLimitCycles;
                 int st = 0;
                 while (true) {
                     if (load_acquire_gpu(&a.cnt->gate_up_done) == items_gu) {
@@ -531,7 +532,7 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate_up,   // u8 [
                         break;
                     }
                     if (load_acquire_gpu(&a.cnt->chunk_done[chunk]) == tiles_gu || abort_raised(abort_flag)) break;
-                    if (clock64() - t0 > kWaitLimitCycles) {
+                    if (clock64() - t0 > lim) {
                         record_status(NF4_ERR_TIMEOUT);
                         *abort_flag = 1;
                         break;
@@ -759,7 +760,7 @@ nf4_moe_experts_kernel(const __grid_constant__ CUtensorMap tm_gate_up,   // u8 [
                 if constexpr (DOWN) {
                     seen = atomicAdd(a.cnt->stripe_done + tile, 1);
                     __threadfence();         // the others' results after it
-                } else {
+                } else if (!g_dbg_skip_flag_set) {
                     atomicAdd(&a.cnt->chunk_done[item_chunk(cur)], 1);
                     atomicAdd(&a.cnt->gate_up_done, 1);
                 }

@@ -143,7 +143,8 @@ __device__ __forceinline__ void mbar_complete_tx(uint64_t *bar, uint32_t bytes) 
 // Test hooks of the stream-K flag wait (set through nf4_debug_flag_wait):
 // when g_dbg_skip_flag_set is nonzero the tails of split tiles do not raise
 // their flags, and a nonzero g_dbg_flag_wait_limit replaces the flag wait's
-// cycle limit, so a test can make that one wait run out.
+// cycle limit, so a test can make that one wait run out; likewise the count of
+// finished gate-up items and the down items' wait for it in the experts kernel.
 __device__ int g_dbg_skip_flag_set;
 __device__ long long g_dbg_flag_wait_limit;
 

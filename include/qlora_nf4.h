@@ -403,6 +403,8 @@ QLORA_API nf4_status nf4_device_status(void *stream);
  * second halves do not signal their partial sums, and limit_cycles > 0
  * replaces that one wait's limit (SM clock cycles), so a test can make it run
  * out in microseconds and check the status and a following clean call.
+ * The same two settings act on nf4_moe_fwd's wait of a down product for its
+ * activations: their completion is not counted, and the wait takes the limit.
  * (0, 0) restores normal operation. Applies to the current device, between
  * calls (it is not ordered with kernels in flight: synchronise first). */
 QLORA_API nf4_status nf4_debug_flag_wait(int32_t skip_flag_set, int64_t limit_cycles);

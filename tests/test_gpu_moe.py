@@ -279,3 +279,26 @@ def test_a_block_as_it_would_be_served(q):
     out, ids, w = q.nf4_moe_fwd(m.gate_up, m.down, stream, m.router, 2, residual=stream, out=stream)
     assert out is stream
     check_moe(q, m, (out, ids, w), "silu", True, m.x)
+
+
+@pytest.mark.parametrize("M,E,k,H,F", [(3, 8, 2, 256, 192), (40, 16, 4, 192, 320)])
+def test_wait_for_activations_runs_out_and_next_call_is_clean(q, M, E, k, H, F):
+    """The gate-up items are not counted, so the down products' wait for them takes
+    its (short) limit: the status says so, and the next call is as ever."""
+    m = Moe(q, M, E, k, H, F)
+    call = lambda: q.nf4_moe_fwd(m.gate_up, m.down, m.x, m.router, k)
+    clean = call()
+    assert q.device_status() == q.NF4_OK
+    try:
+        assert q.lib.nf4_debug_flag_wait(1, 20000) == q.NF4_OK
+        bad = call()
+        torch.cuda.synchronize()
+        st = q.device_status()
+    finally:
+        assert q.lib.nf4_debug_flag_wait(0, 0) == q.NF4_OK
+    assert st == q.NF4_ERR_TIMEOUT, q.status_string(st)
+    assert q.device_status() == q.NF4_OK                  # read once, then cleared
+    assert torch.equal(bad[1], clean[1]) and torch.equal(bad[2], clean[2])    # the routing had no part in it
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(call(), clean))
+    assert q.device_status() == q.NF4_OK
