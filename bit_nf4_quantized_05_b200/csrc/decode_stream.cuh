@@ -33,6 +33,8 @@
 // from bf16(s_b * level) * x by at most one bf16 rounding of each term.
 #pragma once
 
+#include <type_traits>
+
 #include "epilogue.cuh"
 
 namespace nf4 {
@@ -85,8 +87,18 @@ struct DsGroups {
     float gscale[16];
 };
 
-// The output step: none, or EpiArgs (bias, activation, mul, residual).
+// The output step: none, EpiArgs (bias, activation, mul, residual), or EpiArgs
+// with the rows behind `rounds` whole rounds of tiles (one tile a CTA each)
+// dealt out as half tiles of 16 rows, at most one to a CTA. Chosen by the host
+// where those rows fit so: 5120 rows on 144 CTAs are then 1.5 tiles deep
+// instead of 2 (13824 columns: 42.1 -> 37.0 us at 13 tokens, 29.0 -> 26.6 at
+// one; 1024 rows of 4096 columns, one token: 7.8 -> 6.2). A kernel whose tiles
+// divide evenly is faster without the second copy of its loop (13824 rows of
+// 5120 columns, 3 tiles a CTA, one token: 19.7 us, 20.4 with it).
 struct DsNoEpi {};
+struct EpiHalves : EpiArgs {
+    int rounds;
+};
 
 // Table lookup by shared address. The table is written once before a
 // barrier and never again, and every lookup address is derived from code
@@ -161,7 +173,7 @@ struct DsScales {
 // chunk c goes to ring slot c % 2, and the other slot takes chunk c + 1 as soon as
 // every lane has read chunk c.
 // GT: DsNoGroups, or DsGroups for per-token adapter selection.
-// ET: DsNoEpi, or EpiArgs: lane j of a row's half-warp finishes token j, with
+// ET: DsNoEpi, EpiArgs or EpiHalves: lane j of a row's half-warp finishes token j, with
 // its operands fetched at the start of the tile.
 template <int TG, int CB, class GT, class ET>
 __global__ void __launch_bounds__(kDsThreads, 1)
@@ -169,6 +181,7 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
                            const DecodeArgs a, const GT grp, const ET epi) {
     constexpr bool GROUPS = sizeof(GT) > 1;
     constexpr bool EPI = sizeof(ET) > 1;
+    constexpr bool HALVES = std::is_same_v<ET, EpiHalves>;
     extern __shared__ __align__(1024) uint8_t dsm[];
     constexpr uint32_t kSlot = 1024u * CB;           // bytes of one chunk (32 rows x 32 CB)
     constexpr uint32_t kRowStride = 32u * CB;        // bytes per row in a slot
@@ -203,10 +216,25 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
     const int nkb = max(0, min(a.rb, kblocks - kb0));
     const int nch = (nkb + CB - 1) / CB;
     const int ntiles = (Nrows + kDsRows - 1) / kDsRows;
-    const int nt = static_cast<int>(blockIdx.x) < ntiles
-                       ? (ntiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
-                             static_cast<int>(gridDim.x)
-                       : 0;
+    int nt = static_cast<int>(blockIdx.x) < ntiles
+                 ? (ntiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
+                       static_cast<int>(gridDim.x)
+                 : 0;
+    // first row of a half tile, which is a CTA's last
+    [[maybe_unused]] int half_row0 = 0;
+    if constexpr (HALVES) {
+        half_row0 = (epi.rounds * static_cast<int>(gridDim.x) * 2 + static_cast<int>(blockIdx.x)) * 16;
+        nt = epi.rounds + (half_row0 < Nrows ? 1 : 0);
+    }
+    // whether tile ti of this CTA is a half tile: a compile-time false without them
+    auto is_half = [&](int ti) {
+        if constexpr (HALVES) return ti == epi.rounds;
+        else return false;
+    };
+    auto row0_of = [&](int ti) {
+        if (is_half(ti)) return half_row0;
+        return (static_cast<int>(blockIdx.x) + ti * static_cast<int>(gridDim.x)) * kDsRows;
+    };
     const int nchunks = nt * nch;
     // this warp's ring slots: numbered 2 warp, 2 warp + 1 over the window,
     // below the table first
@@ -221,13 +249,12 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
     auto issue = [&](int cc) {
         if (cc >= nchunks || lane != 0) return;
         const int ti = cc / nch, ch = cc - ti * nch;
-        const int tile = static_cast<int>(blockIdx.x) + ti * static_cast<int>(gridDim.x);
         uint64_t *bar = &bars[warp * 2 + (cc & 1)];
         // the slot's previous contents were read through the generic proxy
         fence_proxy_async_smem();
         mbar_arrive_expect_tx(bar, kSlot);
         tma_load_2d(dsm + (((cc & 1) ? slot1 : slot0) - sbase), &tm_codes, bar, (kb0 + ch * CB) * 32,
-                    tile * kDsRows);
+                    row0_of(ti));
     };
 
     // the raw scales of chunk cc for this lane's row
@@ -240,7 +267,7 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
         s.split = CB;
         if (cc >= nchunks) return s;
         const int ti = cc / nch, ch = cc - ti * nch;
-        const int n = (static_cast<int>(blockIdx.x) + ti * static_cast<int>(gridDim.x)) * kDsRows + srow;
+        const int n = row0_of(ti) + srow;
         if (n >= Nrows) return s;
         const int nb = min(CB, nkb - ch * CB);
         const int kbase = kb0 + ch * CB;                 // the chunk's first 64-element step
@@ -320,13 +347,14 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
     constexpr int kParkBufs = TG == 1 ? 2 : 1;
 
     for (int ti = 0; ti < nt; ++ti) {
-        const int tile = static_cast<int>(blockIdx.x) + ti * static_cast<int>(gridDim.x);
+        const bool half = is_half(ti);
         // this lane's share of the LoRA rank columns for the tile's output
         // step, fetched now so the loads are long done by then:
         // B[n][j + 16 i] for row n of half-warp (row, j)
         const int fj = lane & 15;
         const int frow = (warp & 3) + 8 * (warp >> 2) + 4 * ((lane >> 4) & 1);
-        const int fn = tile * kDsRows + frow;
+        // (rows behind a half tile are another CTA's)
+        const int fn = half && frow >= 16 ? Nrows : row0_of(ti) + frow;
         float bq[kDsMaxRank / 16];
 #pragma unroll
         for (int i = 0; i < kDsMaxRank / 16; ++i) {
@@ -378,23 +406,24 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
                                    after_wait_zero();
             const int nbc = min(CB, nkb - ch * CB);
             // one block of the chunk: i is a constant after inlining
-            auto block = [&](const int i) {
+            auto block = [&](const int i, auto groups) {
+                constexpr int RG = decltype(groups)::value;    // 16-row groups of the tile
                 // s[rg][hi] (rows rg*16 + g + 8 hi) comes from lane (g, 2 rg + hi)
-                float s[2][2];
+                float s[RG][2];
 #pragma unroll
-                for (int rg = 0; rg < 2; ++rg)
+                for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
                     for (int hi = 0; hi < 2; ++hi)
                         s[rg][hi] = __shfl_sync(0xffffffffu, s_blk[i], (lane & ~3) | (2 * rg + hi));
 
-                uint2 cw[2][2];    // [rg][hi]: code bytes [8t, 8t+8) of row rg*16 + g + 8 hi
+                uint2 cw[RG][2];    // [rg][hi]: code bytes [8t, 8t+8) of row rg*16 + g + 8 hi
 #pragma unroll
-                for (int rg = 0; rg < 2; ++rg)
+                for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
                     for (int hi = 0; hi < 2; ++hi)
                         cw[rg][hi] = ds_lds64(cbase + (rg * 16 + 8 * hi) * kRowStride + i * 32);
 
-                float pp[2][TG][4];
+                float pp[RG][TG][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     // MMA q covers elements 16t + 4q + {0,1} (slots 2t, 2t+1) and
@@ -407,7 +436,7 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
                         b1[tg] = (q & 1) ? xv.w : xv.y;
                     }
 #pragma unroll
-                    for (int rg = 0; rg < 2; ++rg) {
+                    for (int rg = 0; rg < RG; ++rg) {
                         const uint32_t wl = (q < 2) ? cw[rg][0].x : cw[rg][0].y;
                         const uint32_t wh = (q < 2) ? cw[rg][1].x : cw[rg][1].y;
                         uint32_t af[4];
@@ -430,7 +459,7 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
                     }
                 }
 #pragma unroll
-                for (int rg = 0; rg < 2; ++rg)
+                for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
                     for (int tg = 0; tg < TG; ++tg) {
                         acc[rg][tg][0] = fmaf(s[rg][0], pp[rg][tg][0], acc[rg][tg][0]);
@@ -445,12 +474,16 @@ qlora_decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes,   // [N
                 }
                 load_x(xa1, xb1);
             };
-            if (nbc == CB) {
+            auto blocks = [&](auto groups) {
+                if (nbc == CB) {
 #pragma unroll
-                for (int i = 0; i < CB; ++i) block(i);
-            } else {
-                for (int i = 0; i < nbc; ++i) block(i);
-            }
+                    for (int i = 0; i < CB; ++i) block(i, groups);
+                } else {
+                    for (int i = 0; i < nbc; ++i) block(i, groups);
+                }
+            };
+            if (half) blocks(std::integral_constant<int, 1>{});
+            else blocks(std::integral_constant<int, 2>{});
             __syncwarp();        // every lane has read the chunk
         }
 

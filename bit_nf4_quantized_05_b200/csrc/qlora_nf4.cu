@@ -649,10 +649,14 @@ nf4_status launch_decode(const nf4_weight *w, const uint16_t *x, int64_t M, cons
     if (!make_map(&tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->codes, w->k / 2, w->n,
                   static_cast<uint32_t>(32 * cb), kDsRows, CU_TENSOR_MAP_SWIZZLE_NONE))
         return map_fail(__LINE__);
-    const int64_t tiles = (w->n + kDsRows - 1) / kDsRows;
+    const int64_t tiles = (w->n + kDsRows - 1) / kDsRows, halves = (w->n + kDsRows / 2 - 1) / (kDsRows / 2);
     // the decode grid leaves kDsUCtas SMs to the u kernel
-    const int sms = num_sms(current_device());
-    const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, sms - kDsUCtas)));
+    const int64_t ctas = std::max(1, num_sms(current_device()) - kDsUCtas);
+    // half tiles, with an output step: the rows behind the last whole round
+    // come to at most one half tile a CTA
+    const int64_t hgrid = std::min(halves, ctas), rounds = halves / (2 * hgrid), hrest = halves - 2 * hgrid * rounds;
+    const bool use_halves = epi && hrest > 0 && hrest <= hgrid;
+    const unsigned grid = static_cast<unsigned>(use_halves ? hgrid : std::min(tiles, ctas));
     const int tg = M <= 8 ? 1 : 2;
     {
         // u = x A^T on kDsUCtas CTAs, beside the decode grid
@@ -672,6 +676,9 @@ nf4_status launch_decode(const nf4_weight *w, const uint16_t *x, int64_t M, cons
         gr.ngroups = groups->ngroups;
         for (int i = 0; i < groups->ngroups && i < 16; ++i) gr.gscale[i] = groups->gscale[i];
         e = launch_decode_stream(tg, cb, grid, stream, tm_codes, a, gr);
+    } else if (use_halves) {
+        e = launch_decode_stream(tg, cb, grid, stream, tm_codes, a, DsNoGroups{},
+                                 EpiHalves{*epi, static_cast<int>(rounds)});
     } else if (epi) {
         e = launch_decode_stream(tg, cb, grid, stream, tm_codes, a, DsNoGroups{}, *epi);
     } else {

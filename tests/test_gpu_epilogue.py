@@ -226,6 +226,24 @@ def test_writes_stay_in_their_buffers_and_calls_repeat_bit_for_bit(q, N, K, M, r
         assert torch.equal(t, G[n].t), n
 
 
+@pytest.mark.parametrize("M", [1, 8, 13])
+@pytest.mark.parametrize("N", [24, 2312, 4616, 5128, 6904, 6928, 9232])
+def test_few_tokens_with_every_dealing_of_rows_to_blocks(q, N, M):
+    """Rows in 32- and 16-row tiles over the GPU's blocks: one whole round and a
+    rest, a rest alone, a rest past one half tile each. Each row's sum is taken
+    in the same order whichever it is, so without an epilogue the layer's own
+    kernel, which has 32-row tiles only, gives the same bits."""
+    c = Case(q, N, 320, M, 16, True, 64)
+    want, uw = q.qlora_linear_fwd(c.qw, c.x, c.A, c.B, c.alpha)
+    guard = torch.full((M * N + 512,), -3.0, device="cuda", dtype=torch.bfloat16)
+    out = guard[256:256 + M * N].view(M, N)
+    h, u, _ = q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, save_z=False, h=out)
+    assert torch.equal(h, want) and torch.equal(u, uw)
+    assert (guard[:256] == -3.0).all() and (guard[256 + M * N:] == -3.0).all()
+    h, u, z = q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.bias, "silu", c.mul, c.residual)
+    check_forward(q, c, "silu", "bmr", h, u, z)
+
+
 def test_empty_batch(q):
     c = Case(q, 264, 640, 4, 16)
     e = lambda n: torch.empty(0, n, dtype=torch.bfloat16, device="cuda")
