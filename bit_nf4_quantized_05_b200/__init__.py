@@ -215,7 +215,7 @@ class QuantizedWeight:
     def struct(self) -> NF4WeightStruct:
         self._check_arrays()
         codes, q8, c = self.codes, self.absmax_q8, self.absmax_c
-        return NF4WeightStruct(self.n, self.k, self.block_size, self.double_quant, codes.data_ptr(),
+        return NF4WeightStruct(self.n, self.k, self.block_size, int(self.double_quant), codes.data_ptr(),
                                self.absmax.data_ptr(), None if q8 is None else q8.data_ptr(),
                                None if c is None else c.data_ptr())
 
@@ -228,7 +228,7 @@ class QuantizedWeight:
         if self.block_size not in (64, 128):
             raise ValueError("block_size must be 64 or 128")
         nb = self.n * self.k // self.block_size
-        dev = self.codes.get_device()
+        dev = -1 if self.codes is None else self.codes.get_device()
         self._check_array("codes", self.codes, torch.uint8, self.n * self.k // 2, dev)
         self._check_array("absmax", self.absmax, torch.float32, nb, dev)
         if self.double_quant:

@@ -150,3 +150,15 @@ def test_reference_activations_against_torch():
     for act, ref in (("relu", f.relu), ("silu", f.silu), ("gelu", f.gelu),
                      ("gelu_tanh", lambda t: f.gelu(t, approximate="tanh"))):
         assert float((act64(z, act)[0] - ref(z)).abs().max()) <= 1e-13
+
+
+def test_a_weight_takes_numpy_flags_and_names_the_array_it_lacks(q):
+    import dataclasses
+
+    import numpy as np
+    qw = q.QuantizedWeight.empty(8, 64, True, "cpu")
+    st = dataclasses.replace(qw, double_quant=np.bool_(True)).struct()
+    assert st.double_quant == 1 and st.codes == qw.codes.data_ptr()
+    for name in ("codes", "absmax", "absmax_q8", "absmax_c"):
+        with pytest.raises(ValueError, match=name + " is required"):
+            dataclasses.replace(qw, **{name: None}).struct()
