@@ -472,10 +472,18 @@ __device__ __forceinline__ BlockLut make_block_lut(float s) {
     return block_lut_planes(pair);
 }
 
-// What that rounding left: bf16(s * level - bf16(s * level)). The two tables
-// together hold the fp32 weight to 2^-17.
+// What rounding v to bf16 left, in bf16: the two together hold v to 2^-17. Where the
+// rounded value is not finite there is no rest (the sum would be infinity minus infinity).
+constexpr float kBf16Max = 3.3895313892515355e38f;
+__device__ __forceinline__ float bf16_rest(float v, __nv_bfloat16 rounded) {
+    return fabsf(v) <= kBf16Max ? v - __bfloat162float(rounded) : 0.0f;
+}
+
+// The rests of make_block_lut's entries; none in a block whose scale (the largest entry)
+// is beyond bf16.
 __device__ __forceinline__ BlockLut make_block_lut_rest(float s) {
     uint32_t pair[8];
+    s = fabsf(s) <= kBf16Max ? s : 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float a = s * c_levels[2 * i], b = s * c_levels[2 * i + 1];

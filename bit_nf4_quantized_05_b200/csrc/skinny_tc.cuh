@@ -311,7 +311,7 @@ skinny_cluster_kernel(const __grid_constant__ CUtensorMap tm_a0,
                 __nv_bfloat16 b = __float2bfloat16_rn(sc * acc);
                 J.out_bf16[o] = *reinterpret_cast<uint16_t *>(&b);
                 if (J.out_rest) {
-                    b = __float2bfloat16_rn(sc * acc - __bfloat162float(b));
+                    b = __float2bfloat16_rn(bf16_rest(sc * acc, b));
                     J.out_rest[o] = *reinterpret_cast<uint16_t *>(&b);
                 }
             }

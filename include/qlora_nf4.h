@@ -312,9 +312,12 @@ typedef struct {
  * qlora_fwd_epilogue_workspace_bytes(M, n, k, r) bytes, 256-byte aligned.
  * Otherwise as qlora_linear_fwd, with one difference: for a ReLU with z_out the
  * sum takes the weight and the rank-r activations to 2^-17 instead of bf16's
- * 2^-9 (twice the tensor-core work), because the gradient jumps with the sign
- * of z. No page gives the epilogue: it is the element-wise work that
- * surrounds the pages' layer in a transformer block. */
+ * 2^-8, in two bf16 parts each (twice the tensor-core work, and 1 to 16 tokens
+ * do not take the streaming kernel), because the gradient jumps with the sign of
+ * z. There z of a token with an infinite element is NaN wherever a weight's two
+ * parts have opposite signs. Inference passes no z_out. No page gives the
+ * epilogue: it is the element-wise work that surrounds the pages' layer in a
+ * transformer block. */
 QLORA_API size_t qlora_fwd_epilogue_workspace_bytes(int64_t M, int64_t n, int64_t k, int32_t r);
 QLORA_API nf4_status qlora_linear_fwd_epilogue(const nf4_weight *w, const uint16_t *x, int64_t M,
                                                const uint16_t *A, const uint16_t *B, int32_t r,
