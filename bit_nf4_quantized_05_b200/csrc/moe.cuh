@@ -239,10 +239,10 @@ static_assert(kMoeMaxExperts <= 256 && kMoeMaxTokens <= 64, "ids in a byte, toke
 constexpr int kMoeHeaderBytes = (sizeof(MoeHeader) + 1023) / 1024 * 1024;
 static_assert(kMoeHeaderBytes <= 20 * 1024, "header");
 
-// fp64 values as integers of the same order, from 1 on: NaN is 1, below the rest.
+// fp64 values as integers of the same order, all above 0; NaN as minus infinity.
 __device__ __forceinline__ unsigned long long order_key(double v) {
-    const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v));
-    return isnan(v) ? 1ull : (b >> 63 ? ~b : b | 1ull << 63) + 1ull;
+    const unsigned long long b = isnan(v) ? 0xfff0000000000000ull : static_cast<unsigned long long>(__double_as_longlong(v));
+    return (b >> 63 ? ~b : b | 1ull << 63) + 1ull;
 }
 __device__ __forceinline__ double key_value(unsigned long long key) {
     const unsigned long long b = key - 1ull;
@@ -251,7 +251,7 @@ __device__ __forceinline__ double key_value(unsigned long long key) {
 
 // Routing of all tokens, by every thread of the CTA: the chosen experts with
 // their weights, the chunks, and the slots. Larger logit first, ties to the
-// lower index; a NaN counts as minus infinity (its weights are NaN all the same).
+// lower index; a NaN counts as minus infinity (all weights of its token are NaN).
 // A warp takes a token. A lane counts, for each of its experts, the keys above:
 // by their high words, and by whole keys only where two of those are equal
 // (8 rounds of a warp maximum over 64 experts took twice as long). The
