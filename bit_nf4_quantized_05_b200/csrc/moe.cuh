@@ -48,6 +48,7 @@
 
 #include "decode_stream.cuh"
 #include "epilogue.cuh"
+#include "moe_plan.cuh"
 
 namespace nf4 {
 
@@ -55,10 +56,8 @@ constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 256;
 constexpr int kMoeMaxTopK = 16;
 constexpr int kMoeMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
-constexpr int kMoeChunk = 8;                       // tokens of one work item
 // chunks: every expert's last one may be partly filled
 constexpr int kMoeMaxChunks = kMoeMaxExperts + kMoeMaxSlots / kMoeChunk;
-constexpr int kMoeWarps = 16;
 constexpr int kMoeThreads = 32 * kMoeWarps;
 constexpr int kMoeRows = 64;                       // weight rows of one item
 constexpr int kMoeStepBytes = 64;                  // code bytes of one row in a step: 2 blocks

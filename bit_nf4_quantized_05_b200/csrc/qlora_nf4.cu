@@ -1459,24 +1459,6 @@ bool make_map_3d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t mi
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Warps of a group: the choice with the smallest estimate of (items x (steps of
-// a warp per item + 1) over the groups, plus one item of each kind for the uneven
-// end), the 1 standing for what an item costs beside its steps.
-int pick_moe_group(double chunks, int64_t tiles_gu, int64_t steps_gu, int64_t tiles_dn, int64_t steps_dn, int sms) {
-    int best = 4;
-    double best_cost = -1;
-    for (int gw : {4, 8, 16}) {
-        const double groups = double(sms) * (kMoeWarps / gw);
-        const double gu = double((steps_gu + gw - 1) / gw + 1), dn = double((steps_dn + gw - 1) / gw + 1);
-        const double cost = (chunks * tiles_gu / groups + 1) * gu + (chunks * tiles_dn / groups + 1) * dn;
-        if (best_cost < 0 || cost < best_cost) {
-            best = gw;
-            best_cost = cost;
-        }
-    }
-    return best;
-}
-
 MoeScales moe_scales(const nf4_weight *w) {
     return {w->absmax, w->absmax_q8, w->absmax_c, w->double_quant, block_shift_of(w->block_size)};
 }
@@ -1488,11 +1470,8 @@ nf4_status launch_moe_experts(const nf4_weight *gate_up, const nf4_weight *down,
         !make_map(&tm_dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, down->codes, down->k / 2, down->n, kMoeStepBytes, kMoeRows,
                   CU_TENSOR_MAP_SWIZZLE_64B))
         return map_fail(__LINE__);
-    // at least one chunk per chosen expert; how many experts that is, only the
-    // device knows, so the rule takes the expected number of a router that
-    // spreads its tokens evenly
     const int sms = num_sms(current_device());
-    const double chunks = std::max(1.0, a.E * (1.0 - std::pow(1.0 - double(a.top_k) / a.E, double(a.M))));
+    const double chunks = moe_expected_chunks(a.M, a.E, a.top_k);
     const int gw = pick_moe_group(chunks, a.F / (kMoeRows / 2), (a.H / kBlock + 1) / 2, a.H / kMoeRows,
                                   (a.F / kBlock + 1) / 2, sms);
     auto in_pairs = [](const nf4_weight *w) {
