@@ -3,6 +3,10 @@
 //   forward    z = (the layer's sum) + bias,  h = act(z) . mul + residual
 //   backward   dz = dH . mul . act'(z),  dmul = dH . act(z),  dbias = sum_m dz
 //
+// z is kept in bf16 between the two (half the bytes of the fp32 sum, on a path bound by
+// HBM): act and act' are off by up to 2^-8 |z| times |act'| and |act''|. Only a ReLU's
+// derivative jumps, and the rounding of z does not change its sign.
+//
 // The forward part runs inside the kernels that produce the sum (the fused
 // GEMM's and the decode kernel's output step), on the fp32 accumulator, before
 // its one rounding to bf16. The backward part is the kernel below: its dz

@@ -330,8 +330,9 @@ QLORA_API nf4_status qlora_linear_fwd_epilogue(const nf4_weight *w, const uint16
  *     dmul = dH . act(z),  dbias = sum over tokens of dz (before that rounding)
  *     dX, dA, dB: qlora_linear_bwd of dz;  the residual's gradient is dH itself
  * ep: act and mul as in the forward (bias and residual are not read). z is the
- * forward's z_out; it may be NULL when act is none and dmul is not wanted. u as
- * in qlora_linear_bwd. dX, dbias and dmul may be NULL; dmul needs ep->mul and
+ * forward's z_out, so act and act' are taken at the rounded z: up to 2^-8 |z act'(z)|
+ * and 2^-8 |z act''(z)| from those of the fp32 sum. It may be NULL when act is none
+ * and dmul is not wanted. u as in qlora_linear_bwd. dX, dbias and dmul may be NULL; dmul needs ep->mul and
  * must not overlap dH, z, mul or x, nor dX any of dH, dmul and x
  * (NF4_ERR_INVALID_ARG). With grads_f32 == 1, dA, dB and dbias
  * are fp32, with 0 bf16. relu'(0) = 0. workspace: at least

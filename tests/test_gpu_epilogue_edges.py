@@ -1,9 +1,11 @@
 """The layer with its epilogue where its sums and its kept z are most exposed:
-infinite tokens and overflowing operands under a ReLU that keeps z."""
+infinite tokens and overflowing operands under a ReLU that keeps z, and the
+gradients against the formula at the unrounded z."""
 import pytest
 import torch
 
-from test_gpu_epilogue import q  # noqa: F401
+from epilogue_ref import ACT_EVAL, HALF_BF16, act64, backward64, check, forward64
+from test_gpu_epilogue import ACTS, Case, pick, q  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -80,3 +82,62 @@ def test_scales_beyond_bf16_under_a_relu_that_keeps_z(q, M):
         assert not bool(h[:, [i for i in range(264) if i != 5]].any())
         if save:
             assert bool((z[:, 5] == INF).all()) and bool((z[:, 9] == -INF).all())
+
+
+def curvature(act):
+    """Bounds of |act''| and |act'''| over all z (0 beyond |z| = 14 to 1e-15), from a
+    fine grid; 1% for what lies between its points."""
+    z = torch.linspace(-14, 14, 280001, dtype=torch.float64, requires_grad=True)
+    d2, = torch.autograd.grad(act64(z, act)[1].sum(), z, create_graph=True)
+    d3, = torch.autograd.grad(d2.sum(), z)
+    return 1.01 * float(d2.detach().abs().max()), 1.01 * float(d3.abs().max())
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("N,K,M,r,dq,block", [
+    (264, 640, 5, 16, True, 64), (136, 1152, 16, 64, True, 128), (264, 640, 17, 16, True, 64),
+    (520, 1152, 300, 128, False, 128), (4104, 640, 1100, 16, True, 64),
+])
+def test_gradients_at_the_unrounded_z(q, N, K, M, r, dq, block, act):
+    """Forward and backward together against the formula whose z is never rounded.
+    The kept z is off by d = (the forward's own error) + half a bf16 step of z, so
+    act(z) in dmul is off by |act'| d + max|act''| d^2 / 2 and act'(z) in dz by
+    |act''| d + max|act'''| d^2 / 2: element by element that may be more than dz's own
+    rounding. (A ReLU's sign survives the rounding of z, so act' errs only where |z|
+    is within the forward's error.)"""
+    c = Case(q, N, K, M, r, dq, block)
+    W = q.nf4_dequantize(c.qw, bf16=True)
+    for use in ("b", "bm"):
+        bias, mul, _ = pick(c, use)
+        h, u, z = q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, bias, act, mul)
+        got = q.qlora_linear_bwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.dH, z, act, mul, u=u, need_dbias=True)
+        exact = act == "relu"
+        _, z64, _, tol = forward64(c.operand(q, exact), c.x, c.A, c.B, c.s, bias, act, mul, None, exact)
+        want = backward64(W, c.x, c.A, c.B, c.s, c.dH, z64, act, mul, u)
+        d = tol + HALF_BF16 * (z64.abs() + tol)
+        dH, ma = c.dH.double().abs(), 1.0 if mul is None else mul.double().abs()
+        if act == "none":
+            e0, e1 = d, torch.zeros_like(d)
+        elif act == "relu":
+            e0, e1 = d, (z64.abs() <= tol).double()
+        else:
+            top2, top3 = curvature(act)
+            zz = z64.detach().requires_grad_()
+            d2, = torch.autograd.grad(act64(zz, act)[1].sum(), zz)
+            e0 = act64(z64, act)[1].abs() * d + top2 / 2 * d * d
+            e1 = d2.abs() * d + top3 / 2 * d * d
+        # (evaluated at the kept z, which is up to d larger)
+        ev = 0.0 if act in ("none", "relu") else ACT_EVAL
+        ez = dH * ma * (e1 + ev * d)                                # of dz before its rounding
+        er = ez * (1 + HALF_BF16)
+        A, B, x = (t.double().abs() for t in (c.A, c.B, c.x))
+        s = abs(c.s)
+        # (rounding of s v, and the fp32 sums, act on the error's own share too)
+        more = 1 + HALF_BF16 + (N + K + M + r + 16) * 2.0 ** -23
+        eb = (er @ B) * more
+        extra = dict(dX=(er @ W.double().abs() + s * eb @ A) * more, dA=s * (eb.T @ x) * more,
+                     dB=s * (er.T @ u.double().abs()) * more, dbias=ez.sum(0) * more,
+                     dmul=dH * (e0 + ev * d))
+        for name, t in zip(("dX", "dA", "dB", "dbias", "dmul"), got):
+            if t is not None:
+                check(name, t, want[name][0], want[name][1] + extra[name])
