@@ -1,11 +1,12 @@
 """The layer with its epilogue where its sums and its kept z are most exposed:
-infinite tokens and overflowing operands under a ReLU that keeps z, and the
-gradients against the formula at the unrounded z."""
+infinite tokens and overflowing operands under a ReLU that keeps z, the
+gradients against the formula at the unrounded z, the wider
+GEMM tiles, and every form of the streaming kernel."""
 import pytest
 import torch
 
 from epilogue_ref import ACT_EVAL, HALF_BF16, act64, backward64, check, forward64
-from test_gpu_epilogue import ACTS, Case, pick, q  # noqa: F401
+from test_gpu_epilogue import ACTS, Case, check_forward, pick, q  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -141,3 +142,36 @@ def test_gradients_at_the_unrounded_z(q, N, K, M, r, dq, block, act):
         for name, t in zip(("dX", "dA", "dB", "dbias", "dmul"), got):
             if t is not None:
                 check(name, t, want[name][0], want[name][1] + extra[name])
+
+
+# 192-wide tiles in one round of CTA pairs, and whole 256-wide tiles in one round
+# (the other shapes of the tests take 128-wide tiles, or split 256-wide ones)
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+@pytest.mark.parametrize("N,M", [(4104, 513), (5120, 517)])
+def test_wider_tiles(q, N, M, act):
+    c = Case(q, N, 320, M, 24)
+    for use in ("bmr", ""):
+        bias, mul, residual = pick(c, use)
+        for save in (True, False):
+            h, u, z = q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, bias, act, mul, residual, save_z=save)
+            check_forward(q, c, act, use, h, u, z)
+    h, u, z = q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.bias, act, c.mul)
+    got = q.qlora_linear_bwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.dH, z, act, c.mul, u=u, need_dbias=True)
+    want = backward64(q.nf4_dequantize(c.qw, bf16=True), c.x, c.A, c.B, c.s, c.dH, z, act, c.mul, u)
+    for name, t in zip(("dX", "dA", "dB", "dbias", "dmul"), got):
+        check(name, t, *want[name])
+    inplace = c.residual.clone()
+    h, _, _ = q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.bias, act, c.mul, inplace, h=inplace)
+    assert torch.equal(h, q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.bias, act, c.mul, c.residual)[0])
+    assert q.device_status() == q.NF4_OK
+
+
+# every chunk width of the streaming kernel (1 to 5 blocks, from K), up to 8 and up to 16
+# tokens, with half tiles (24 rows) and without (4608 rows: whole tiles on 144 CTAs)
+@pytest.mark.parametrize("K", [640, 1152, 2560, 4096, 5120])
+@pytest.mark.parametrize("N,M", [(24, 3), (24, 13), (4608, 3), (4608, 13)])
+def test_every_chunk_width_of_few_tokens(q, N, M, K):
+    c = Case(q, N, K, M, 16)
+    h, u, z = q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.bias, "silu", c.mul, c.residual)
+    check_forward(q, c, "silu", "bmr", h, u, z)
+    assert q.device_status() == q.NF4_OK
