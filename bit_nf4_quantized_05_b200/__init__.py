@@ -619,8 +619,9 @@ def qlora_linear_fwd_epilogue(qw: QuantizedWeight, x: torch.Tensor, A: torch.Ten
     ACTIVATIONS. h may be the residual (or mul) itself. Returns (h, u, z) with
     u = x A^T (fp32) if save_u and the pre-activation z (bf16) if save_z: what
     qlora_linear_bwd_epilogue takes. For act "relu" with save_z the sum is formed
-    more exactly, at twice the products (see the C header). workspace: at least
-    fwd_epilogue_workspace_bytes."""
+    more exactly, at twice the products and, for 1 to 16 tokens, without the
+    few-token kernel (see the C header): pass save_z=False where no backward
+    follows. workspace: at least fwd_epilogue_workspace_bytes."""
     M, r, dev = _layer_fast(qw, x, A, B)
     ep = _epilogue(qw, M, act, bias, mul, residual, dev)
     _check_fast("h", h, (M, qw.n), torch.bfloat16, qw, dev)

@@ -94,7 +94,8 @@ struct DsGroups {
 // instead of 2 (13824 columns: 42.1 -> 37.0 us at 13 tokens, 29.0 -> 26.6 at
 // one; 1024 rows of 4096 columns, one token: 7.8 -> 6.2). A kernel whose tiles
 // divide evenly is faster without the second copy of its loop (13824 rows of
-// 5120 columns, 3 tiles a CTA, one token: 19.7 us, 20.4 with it).
+// 5120 columns, 3 tiles a CTA, one token: 19.7 us, 20.4 with it). The one tensor map
+// has whole tiles' boxes, so a half tile's 32 rows are fetched and 16 used.
 struct DsNoEpi {};
 struct EpiHalves : EpiArgs {
     int rounds;

@@ -27,10 +27,12 @@ struct EpiArgs {
 
 // ---------------------------------------------------------------------------
 // Activations in fp32. The logistic function comes from the hardware
-// exponential and division (a few 2^-22 relative), far inside the bf16
-// rounding of every result; both GELU forms go through functions that keep
-// their relative accuracy for large negative z (no 1 + tanh or 1 + erf
-// cancellation). NaN passes through every activation.
+// exponential and division: a few 2^-22 relative, and |z| 2^-23 more from the
+// rounding of the exponential's argument (2^-16 at |z| = 100), far inside the
+// bf16 rounding (2^-8) of every result; below z = -87.3, where it is under 2^-126, it is 0
+// (the division's range). Both GELU forms go through functions
+// without a cancellation (1 + tanh, 1 + erf) for large negative z. NaN passes
+// through every activation.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
@@ -39,9 +41,12 @@ constexpr float kGeluTanhCubic = 0.044715f;
 
 // Normal distribution function. With x = |z| / sqrt 2 and t = 1 / (1 + x / 2),
 //   erfc(x) = t 2^(-x^2 log2(e) + Q(t)),
-// where Q is a degree-7 Chebyshev fit of log2(erfc(x) e^(x^2) / t) over
-// 0.08 <= t <= 1: 1e-6 relative, also where erfc itself is tiny (beyond |z| =
-// 32 both are 0 in fp32). One reciprocal, one exponential and eight multiply-adds.
+// the form of Press, Teukolsky, Vetterling and Flannery, Numerical Recipes, section
+// 6.2 (erfcc); Q is a degree-7 Chebyshev fit of log2(erfc(x) e^(x^2) / t) over
+// 0.08 <= t <= 1, made here. Relative error, with every operation rounded once: 1e-6 for
+// z > -3; below, the rounding of the exponent (which grows as z^2) adds to it, 2e-6 down to
+// -6, 3.3e-6 to -9, 8.5e-6 to -13 (beyond |z| = 32 both are 0 in fp32). One reciprocal,
+// one exponential and eight multiply-adds.
 __device__ __forceinline__ float normal_cdf(float z) {
     const float t = __fdividef(1.0f, fmaf(0.35355339059327376f, fabsf(z), 1.0f));
     float q = -0.27331653237342834f;

@@ -36,11 +36,12 @@
 // What bounds it: some 300 SM cycles per 4 KB of codes (4.0 TB/s over the card)
 // against 178 at HBM's rate. The shared-memory pipe takes 235 to 268 wavefronts of
 // them (128 table lookups, 32 for the codes, 16 shuffles of scales, operands, sums),
-// but leaving out any one part saves a tenth at most. Around that, a call spends
+// but leaving out any one part saves an eighth at most. Around that, a call spends
 // about 12 us on router, routing and the first codes, and one item's time at the
-// uneven end: 24 us for one token at 8 of 64 experts (2048, 1024; 25 MB of codes),
-// 213 us for 4 tokens at 2 of 8 (5120, 13824; 600 MB), 93 us for 16 tokens at 6 of
-// 64 (2048, 1408; 234 MB).
+// uneven end: 24 us for one token at 8 of 64 experts (2048, 1024; 25 MB of codes);
+// 171, 195 or 224 us for 4 tokens at 2 of 8 (5120, 13824), as they come to 5, 6 or 7
+// different experts of 108 MB each; 94 us for 16 tokens at 6 of 64 (2048, 1408; 54
+// experts, 241 MB).
 #pragma once
 
 #include <cstddef>
