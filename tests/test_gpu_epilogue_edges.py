@@ -175,3 +175,42 @@ def test_every_chunk_width_of_few_tokens(q, N, M, K):
     h, u, z = q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.bias, "silu", c.mul, c.residual)
     check_forward(q, c, "silu", "bmr", h, u, z)
     assert q.device_status() == q.NF4_OK
+
+
+def test_offsets_past_32_bits(q):
+    """More than 2^31 elements in h, z, mul, the residual and the gradients: rows at the
+    start, around element 2^31 and at the end against the formula, dbias over all rows."""
+    N, K, M, r = 28672, 128, 75009, 8
+    c = Case(q, N, K, 32, r)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    mk = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)
+    c.M, c.x, c.mul, c.residual, c.dH = M, mk(M, K), mk(M, N), mk(M, N), mk(M, N)
+    W = q.nf4_dequantize(c.qw, bf16=True)
+    at = 2 ** 31 // N
+    for act in ("silu", "relu"):
+        h, u, z = q.qlora_linear_fwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.bias, act, c.mul, c.residual)
+        dX, _, _, dbias, dmul = q.qlora_linear_bwd_epilogue(c.qw, c.x, c.A, c.B, c.alpha, c.dH, z, act, c.mul, u=u,
+                                                            need_dbias=True, grad_dtype=torch.float32)
+        for i in (0, at - 20, M - 40):
+            s = slice(i, i + 40)
+            p = Case.__new__(Case)
+            p.__dict__.update(c.__dict__, M=M, x=c.x[s], mul=c.mul[s], residual=c.residual[s])
+            check_forward(q, p, act, "bmr", h[s], u[s], z[s])
+            want = backward64(W, c.x[s], c.A, c.B, c.s, c.dH[s], z[s], act, c.mul[s], u[s])
+            check("dX", dX[s], *want["dX"])
+            check("dmul", dmul[s], *want["dmul"])
+        total, size = torch.zeros(N, dtype=torch.float64, device="cuda"), torch.zeros(N, dtype=torch.float64, device="cuda")
+        err = torch.zeros_like(total)
+        for i in range(0, M, 5000):
+            s = slice(i, i + 5000)
+            z64 = z[s].double()
+            dz = c.dH[s].double() * act64(z64, act)[1] * c.mul[s].double()
+            total += dz.sum(0)
+            size += dz.abs().sum(0)
+            if act == "silu":
+                err += (c.dH[s].double() * c.mul[s].double() * z64.abs().clamp_min(1)).abs().sum(0) * ACT_EVAL
+            del z64, dz
+        # fp32 sums of at most M terms in some order
+        check("dbias", dbias, total, err + (M + 4) * 2.0 ** -24 * size, out_half=2.0 ** -24)
+        del h, u, z, dX, dbias, dmul
+    assert q.device_status() == q.NF4_OK
