@@ -67,3 +67,27 @@ def test_against_the_nf4_levels(q, act, block, dq):
     assert rel <= (0.00083 ** 2 * (1.1 ** 2 + 2) + 2 * 2.0 ** -16 / 3) ** 0.5, rel
     along = ((got * want).sum() / (want * want).sum()).item() - 1
     assert abs(along) <= 3 * (6.1e-5 if block == 128 else 1e-6) + 5 * 0.0035 / (48 * 1024) ** 0.5, along
+
+
+@pytest.mark.parametrize("M,E,k,H,F", [(64, 32, 8, 256, 256), (5, 8, 2, 640, 320), (37, 4, 3, 1216, 1024)])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_the_output_over_the_tokens(q, M, E, k, H, F, with_residual):
+    """out may be x, alone or with x as the residual; also captured, where each replay
+    takes the output before as its tokens."""
+    m = Moe(q, M, E, k, H, F)
+    step = lambda x, out: q.nf4_moe_fwd(m.gate_up, m.down, x, m.router, k, residual=x if with_residual else None, out=out)
+    want = [m.x]
+    for _ in range(4):
+        want.append(step(want[-1], None)[0])
+    x = m.x.clone()
+    for w in want[1:]:
+        assert step(x, x)[0] is x and torch.equal(x, w)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(x, x)
+    x.copy_(m.x)
+    for w in want[1:]:
+        g.replay()
+        assert torch.equal(x, w)
+    assert q.device_status() == q.NF4_OK
