@@ -704,7 +704,7 @@ def nf4_moe_fwd(gate_up: QuantizedWeight, down: QuantizedWeight, x: torch.Tensor
     rule. out may be the residual itself, and x."""
     if x.dim() != 2 or router.dim() != 2:
         raise ValueError("x and router must be 2-D")
-    k, top_k = top_k, int(top_k)               # any integer type; a fraction is refused, not cut off
+    k, top_k = top_k, int(top_k)               # any number type; a fraction is refused, not cut off
     if top_k != k:
         raise ValueError(f"top_k must be an integer, got {k!r}")
     M, H, E, dev = x.shape[0], gate_up.k, router.shape[0], gate_up.codes.get_device()

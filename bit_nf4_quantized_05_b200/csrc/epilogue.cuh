@@ -29,8 +29,8 @@ struct EpiArgs {
 // Activations in fp32. The logistic function comes from the hardware
 // exponential and division: a few 2^-22 relative, and |z| 2^-23 more from the
 // rounding of the exponential's argument (2^-16 at |z| = 100), far inside the
-// bf16 rounding (2^-8) of every result; below z = -87.3, where it is under 2^-126, it is 0
-// (the division's range). Both GELU forms go through functions
+// bf16 rounding (2^-8) of every result; below z = -87.3, where it is under
+// 2^-126, it is 0 (the division's range). Both GELU forms go through functions
 // without a cancellation (1 + tanh, 1 + erf) for large negative z. NaN passes
 // through every activation.
 // ---------------------------------------------------------------------------

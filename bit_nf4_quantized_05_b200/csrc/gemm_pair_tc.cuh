@@ -271,7 +271,7 @@ __device__ __forceinline__ void set_flag_gpu(int *flag) {
 // needs that: an error d in z turns the sign of a share d / (3 std(z)) of the
 // elements, and each of those is wrong by its whole size (at 5120 x 5120, one
 // pass left dX 3.2% off in the 2-norm, two leave it near its output's rounding). An
-// infinite activation times two parts of opposite sign is NaN; parts of one sign (cut
+// infinite activation times two parts of opposite sign (or a rest of 0) is NaN; parts of one sign (cut
 // off instead of rounded) would avoid that, but hold one bit less: dX, dA and dB were then
 // 0.36% off instead of 0.27%, and the forward took 253 us instead of 245 (2048 tokens).
 template <int BN, bool DGRAD, int G, bool OUT32, bool EPI = false, bool TWICE = false>

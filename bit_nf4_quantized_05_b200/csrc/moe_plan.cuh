@@ -12,7 +12,7 @@ constexpr int kMoeChunk = 8;                       // tokens of one work item
 constexpr int kMoeWarps = 16;                      // of a CTA
 
 // Expected number of chunks (up to kMoeChunk tokens of one expert) of a router that
-// spreads its tokens evenly: E sum over j >= 0 of P(n > kMoeChunk j), n the tokens of an
+// spreads its tokens evenly: E times the mean of ceil(n / kMoeChunk), n the tokens of an
 // expert, binomial in M tokens of probability top_k / E. How many there are in a call,
 // only the device knows.
 inline double moe_expected_chunks(int M, int E, int top_k) {
@@ -31,8 +31,8 @@ inline double moe_expected_chunks(int M, int E, int top_k) {
 // end), the 1 standing for what an item costs beside its steps. Small groups are ahead
 // where there are many items (us with 4 / 8 / 16 warps: 64 tokens at 8 of 32 experts,
 // 2048 x 1024, 112 / 115 / 149), larger ones where few items are left to the end (64 at
-// 2 of 8, 59 / 50 / 55; 3 at 2 of 8, 5120 x 2112, 52 / 45 / 40). Over 46 measured shapes,
-// 24 of them drawn after the 1.75 was set, the choice is 0.8% above the best of the three in
+// 2 of 8, 59 / 50 / 55; 3 at 2 of 8, 5120 x 2112, 52 / 45 / 40). Over 46 measurements,
+// 18 at shapes drawn after the 1.75 was set, the choice is 0.8% above the best of the three in
 // the mean and 13% at worst (4 tokens at 2 of 96, 1408 x 3456: 16 warps 46, 8 warps 41); with
 // the number of chosen experts for the chunks and 1 for the 1.75 it was 2.5% and 22%.
 inline int pick_moe_group(double chunks, int64_t tiles_gu, int64_t steps_gu, int64_t tiles_dn, int64_t steps_dn, int sms) {

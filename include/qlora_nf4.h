@@ -314,8 +314,8 @@ typedef struct {
  * sum takes the weight and the rank-r activations to 2^-17 instead of bf16's
  * 2^-8, in two bf16 parts each (twice the tensor-core work, and 1 to 16 tokens
  * do not take the streaming kernel), because the gradient jumps with the sign of
- * z. There z of a token with an infinite element is NaN wherever a weight's two
- * parts have opposite signs. Inference passes no z_out. No page gives the
+ * z. There z of a token with an infinite element is NaN wherever a weight's second
+ * part is zero or has the other sign. Inference passes no z_out. No page gives the
  * epilogue: it is the element-wise work that surrounds the pages' layer in a
  * transformer block. */
 QLORA_API size_t qlora_fwd_epilogue_workspace_bytes(int64_t M, int64_t n, int64_t k, int32_t r);
@@ -332,10 +332,10 @@ QLORA_API nf4_status qlora_linear_fwd_epilogue(const nf4_weight *w, const uint16
  * ep: act and mul as in the forward (bias and residual are not read). z is the
  * forward's z_out, so act and act' are taken at the rounded z: up to 2^-8 |z act'(z)|
  * and 2^-8 |z act''(z)| from those of the fp32 sum. It may be NULL when act is none
- * and dmul is not wanted. u as in qlora_linear_bwd. dX, dbias and dmul may be NULL; dmul needs ep->mul and
- * must not overlap dH, z, mul or x, nor dX any of dH, dmul and x
- * (NF4_ERR_INVALID_ARG). With grads_f32 == 1, dA, dB and dbias
- * are fp32, with 0 bf16. relu'(0) = 0. workspace: at least
+ * and dmul is not wanted. u as in qlora_linear_bwd. dX, dbias and dmul may be NULL;
+ * dmul needs ep->mul and must not overlap dH, z, mul or x, nor dX any of dH, dmul
+ * and x (NF4_ERR_INVALID_ARG). With grads_f32 == 1, dA, dB and dbias are fp32, with
+ * 0 bf16. relu'(0) = 0. workspace: at least
  * qlora_bwd_epilogue_workspace_bytes(M, n, k, r) bytes, 256-byte aligned. M == 0
  * writes zeros to dA, dB and dbias. */
 QLORA_API size_t qlora_bwd_epilogue_workspace_bytes(int64_t M, int64_t n, int64_t k, int32_t r);

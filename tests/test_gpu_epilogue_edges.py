@@ -1,7 +1,7 @@
 """The layer with its epilogue where its sums and its kept z are most exposed:
 infinite tokens and overflowing operands under a ReLU that keeps z, the
-gradients against the formula at the unrounded z, the wider
-GEMM tiles, and every form of the streaming kernel."""
+gradients against the formula at the unrounded z, the wider GEMM tiles, every
+form of the streaming kernel, and offsets past 32 bits."""
 import pytest
 import torch
 
@@ -34,8 +34,8 @@ class Plain:
 @pytest.mark.parametrize("inf", [INF, -INF])
 @pytest.mark.parametrize("N,K,M", [(264, 640, 5), (264, 640, 150), (4104, 320, 1100)])
 def test_an_infinite_token_under_a_relu_that_keeps_z(q, N, K, M, inf):
-    """Its z is the infinity that one pass gives, or NaN (where the two parts of the
-    weight differ in sign); the other tokens keep their bits."""
+    """Its z is the infinity that one pass gives, or NaN (where the weight's rest is zero
+    or of the other sign); the other tokens keep their bits."""
     c = Plain(q, N, K, M, 16, 2.0)
     c.A[:, 100] = 2.0 ** -6
     c.x[3] = 0

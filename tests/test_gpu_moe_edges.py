@@ -1,5 +1,6 @@
 """The mixture of NF4 experts: routing of logits that are no numbers, every group
-size, and the products against the weights that the NF4 levels define."""
+size, the products against the weights that the NF4 levels define, and the output
+over the tokens."""
 import pytest
 import torch
 
